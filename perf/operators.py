@@ -116,7 +116,8 @@ def work(case):
         # q, dO, o, lse, dq once each; k, v, dk, dv once each (the forward's o and lse stay in the output)
         return {"bytes": rows * (4 * d * 2 + 4) + kv * 4 * d * 2, "flops": 14 * d * pairs}
     if c["kind"] == "write":
-        rows = 2 * c["B"] * c["Hkv"] * c["T"]
+        # the numbers of new rows are uniform in [max(1, T / 2), T]
+        rows = c["B"] * c["Hkv"] * (max(1, c["T"] // 2) + c["T"])
         packed = d // 2 + 2 * (d // GROUP)
         return {"bytes": rows * (2 * d * 2 + packed), "flops": 4 * d * rows}
     # lengths are uniform in [lmin, Lmax]

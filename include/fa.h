@@ -208,6 +208,35 @@ FA_API fa_status fa_bwd_deterministic(const void* q, const void* k, const void* 
                  void* stream);
 
 /*
+ * Sliding-window attention with sinks, and key/value heads shared by several query heads.
+ *
+ * Query row i sits at position p = i + (Nk - Nq) (the causal alignment of fa_fwd).  Key j is visible to
+ * it iff j <= p and (j > p - window or j < sinks): the last `window` keys up to and including its own
+ * position, and the first `sinks` keys of the sequence, which never leave the view.  window >= Nk is
+ * plain causal attention; sinks = 0 is a plain sliding window.
+ *
+ *   q, o, dO, dq  [B, H, Nq, d] bf16;  lse [B, H, Nq] fp32
+ *   k, v, dk, dv  [B, Hkv, Nk, d] bf16; Hkv divides H, and query head h reads key/value head
+ *                 h / (H / Hkv), whose gradients sum over its query heads
+ *   window >= 1, sinks >= 0 (FA_ERR_INVALID_ARG otherwise); Nq and Nk as in fa_fwd
+ *   workspace     at least fa_bwd_window_workspace_size() bytes, 256-byte aligned; contents on entry
+ *                 ignored, garbage on exit (0 where the sizes are invalid or there is no query row)
+ * A row that sees no key (p < 0) gets O = 0, LSE = -inf and dq = 0; a key that no row sees gets
+ * dk = dv = 0.  A key tile (128 keys) is read whole: K and V must be finite in every tile that a row sees
+ * a key of, the hidden keys of those tiles included.  Tiles that no row of a 256-row block sees cost it
+ * nothing: the work follows the window, not Nk.  dk and dv are bitwise reproducible; dq sums meet through
+ * reduce-adds as in fa_bwd.  Other conventions and limits are those of fa_fwd / fa_bwd.
+ */
+FA_API fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse,
+                               int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks,
+                               float scale, void* stream);
+FA_API size_t fa_bwd_window_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks);
+FA_API fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                               const float* lse, void* dq, void* dk, void* dv, void* workspace,
+                               size_t ws_bytes, int B, int H, int Hkv, int Nq, int Nk, int d, int window,
+                               int sinks, float scale, void* stream);
+
+/*
  * Bytes of workspace fa_decode_splitkv needs for the per-split partial
  * results (m, l, unnormalised O) at the given split count (0 = the automatic
  * choice for this Lmax).  Returns 0 on invalid sizes.

@@ -9,9 +9,10 @@ C-ABI mirrors (same names, torch tensors in place of pointers):
     fa_fwd, fa_bwd, fa_bwd_deterministic, fa_bwd_workspace_size, fa_decode_splitkv, fa_decode_num_splits,
     fa_decode_partials, fa_decode_merge,
     fa_decode_workspace_size, fa_decode_splitkv_noalloc, fa_quantize_fp8, fa_fwd_fp8, fa_fwd_ext,
-    fa_bwd_ext, fa_get_device_error, fa_debug_set_wait_limit, fa_status_string, fa_version
+    fa_bwd_ext, fa_fwd_window, fa_bwd_window, fa_bwd_window_workspace_size, fa_get_device_error, fa_debug_set_wait_limit, fa_status_string, fa_version
 Convenience wrappers that allocate outputs:
-    attention_forward, attention_backward, decode_splitkv, quantize_fp8, attention_forward_fp8
+    attention_forward, attention_backward, decode_splitkv, quantize_fp8, attention_forward_fp8,
+    attention_forward_window, attention_backward_window
 """
 from __future__ import annotations
 
@@ -27,6 +28,8 @@ __all__ = [
     "fa_get_device_error", "fa_debug_set_wait_limit", "fa_status_string",
     "fa_version", "attention_forward", "attention_backward", "decode_splitkv", "quantize_fp8",
     "attention_forward_fp8",
+    "fa_fwd_window", "fa_bwd_window", "fa_bwd_window_workspace_size",
+    "attention_forward_window", "attention_backward_window",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -85,6 +88,12 @@ def lib() -> ctypes.CDLL:
     L.fa_bwd_ext.argtypes = [vp, vp, vp, vp, vp, vp, vp, i, i, vp, vp, vp, vp, sz, i, i, i, i, i, f, i, f, u64, u32,
                              vp]
     L.fa_bwd_ext.restype = i
+    L.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, i, i, i, f, vp]
+    L.fa_fwd_window.restype = i
+    L.fa_bwd_window_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+    L.fa_bwd_window_workspace_size.restype = sz
+    L.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, i, i, i, f, vp]
+    L.fa_bwd_window.restype = i
     L.fa_debug_set_wait_limit.argtypes = [ctypes.c_ulonglong]
     L.fa_debug_set_wait_limit.restype = i
     L.fa_get_device_error.argtypes = [vp]
@@ -395,6 +404,68 @@ def fa_fwd_fp8(q8, k8, v8, descale_q, descale_k, descale_v, o, lse, causal: bool
                                 _stream_ptr(stream, dev)), "fa_fwd_fp8")
 
 
+def _window_args(window, sinks):
+    """The C ABI's window and sinks from Python integers (the C ABI clamps both to the keys there are)."""
+    window, sinks = int(window), int(sinks)
+    if window < 1 or sinks < 0:
+        raise ValueError(f"window must be at least 1 and sinks at least 0, got {window} and {sinks}")
+    return min(window, 0x7FFFFFFF), min(sinks, 0x7FFFFFFF)
+
+
+def _kv_heads(k, H, B, d):
+    """Hkv and Nk of k [B, Hkv, Nk, d], whose heads each serve H / Hkv query heads."""
+    if k.dim() != 4 or k.shape[0] != B or k.shape[3] != d:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected [{B}, Hkv, Nk, {d}]")
+    Hkv = k.shape[1]
+    if H % Hkv if Hkv else H:
+        raise ValueError(f"{H} query heads cannot share {Hkv} key/value heads")
+    return Hkv, k.shape[2]
+
+
+def fa_fwd_window(q, k, v, o, lse, window: int, sinks: int = 0, scale=None, stream=None) -> None:
+    """Sliding-window forward with sinks and shared key/value heads (see include/fa.h: fa_fwd_window).
+    q/o [B,H,Nq,d], k/v [B,Hkv,Nk,d] bf16, lse [B,H,Nq] fp32."""
+    import torch
+    B, H, Nq, d = q.shape
+    Hkv, Nk = _kv_heads(k, H, B, d)
+    window, sinks = _window_args(window, sinks)
+    dev = q.device
+    _need(q, "q", torch.bfloat16, dev)
+    _need(k, "k", torch.bfloat16, dev)
+    _need(v, "v", torch.bfloat16, dev, (B, Hkv, Nk, d))
+    _need(o, "o", torch.bfloat16, dev, (B, H, Nq, d))
+    _need(lse, "lse", torch.float32, dev, (B, H, Nq))
+    with _on_device(dev):
+        _check(lib().fa_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Hkv, Nq, Nk, d, window, sinks,
+                                   _scale(scale, d), _stream_ptr(stream, dev)), "fa_fwd_window")
+
+
+def fa_bwd_window_workspace_size(B: int, H: int, Hkv: int, Nq: int, Nk: int, d: int, window: int,
+                                 sinks: int = 0) -> int:
+    return int(lib().fa_bwd_window_workspace_size(B, H, Hkv, Nq, Nk, d, *_window_args(window, sinks)))
+
+
+def fa_bwd_window(q, k, v, o, dO, lse, dq, dk, dv, workspace, window: int, sinks: int = 0, scale=None,
+                  stream=None) -> None:
+    """Backward of fa_fwd_window (see include/fa.h: fa_bwd_window); dk and dv [B,Hkv,Nk,d] sum over the query heads
+    that share a key/value head.  workspace: uint8 device tensor."""
+    import torch
+    B, H, Nq, d = q.shape
+    Hkv, Nk = _kv_heads(k, H, B, d)
+    window, sinks = _window_args(window, sinks)
+    dev = q.device
+    for t, n, shp in ((q, "q", (B, H, Nq, d)), (o, "o", (B, H, Nq, d)), (dO, "dO", (B, H, Nq, d)),
+                      (dq, "dq", (B, H, Nq, d)), (k, "k", (B, Hkv, Nk, d)), (v, "v", (B, Hkv, Nk, d)),
+                      (dk, "dk", (B, Hkv, Nk, d)), (dv, "dv", (B, Hkv, Nk, d))):
+        _need(t, n, torch.bfloat16, dev, shp)
+    _need(lse, "lse", torch.float32, dev, (B, H, Nq))
+    _need(workspace, "workspace", torch.uint8, dev)
+    with _on_device(dev):
+        _check(lib().fa_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+                                   _ptr(workspace), workspace.numel(), B, H, Hkv, Nq, Nk, d, window, sinks,
+                                   _scale(scale, d), _stream_ptr(stream, dev)), "fa_bwd_window")
+
+
 def fa_debug_set_wait_limit(limit_ns: int, device=None) -> None:
     """Test hook (see include/fa.h: fa_debug_set_wait_limit): the limit of every pipeline wait on
     ``device`` (default: current), 0 restoring the default 2 s."""
@@ -475,3 +546,28 @@ def attention_forward_fp8(q, k, v, causal: bool = False, scale=None, signs=None,
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     fa_fwd_fp8(q8, k8, v8, dq, dk, dv, o, lse, causal, scale, stream)
     return o, lse
+
+
+def attention_forward_window(q, k, v, window: int, sinks: int = 0, scale=None, stream=None):
+    """Allocate O and LSE and run fa_fwd_window; returns (o, lse)."""
+    import torch
+    B, H, Nq, d = q.shape
+    o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stream)
+    return o, lse
+
+
+def attention_backward_window(q, k, v, o, lse, dO, window: int, sinks: int = 0, scale=None, stream=None,
+                              workspace=None):
+    """Allocate dQ, dK, dV (and the workspace unless given) and run fa_bwd_window; returns (dq, dk, dv)."""
+    import torch
+    B, H, Nq, d = q.shape
+    dq = torch.empty_like(q)
+    dk = torch.empty_like(k)
+    dv = torch.empty_like(v)
+    if workspace is None:
+        Hkv, Nk = _kv_heads(k, H, B, d)
+        workspace = _workspace(fa_bwd_window_workspace_size(B, H, Hkv, Nq, Nk, d, window, sinks), q.device)
+    fa_bwd_window(q, k, v, o, dO, lse, dq, dk, dv, workspace, window, sinks, scale, stream)
+    return dq, dk, dv

@@ -118,6 +118,12 @@ struct BwdParams {
   int bias_pb, bias_ph;
   int H;
   DropoutCfg drop;
+  // Sliding-window instantiation only (visibility as in FwdParams).  BH counts key/value heads here, each
+  // shared by `group` query heads; the first ns key tiles hold the sink keys, which every later query
+  // sees: their query blocks are cut into `parts` shares of plen blocks, one CTA each, whose fp32
+  // partial dV and dK go to `part` [BH, ns, parts, 2, 128, D] (parts = 1: no cut, written directly).
+  int window, sinks, group, ns, parts, plen;
+  float* part;
 };
 
 // ---------------------------------------------------------------------------------------------
@@ -173,6 +179,42 @@ __device__ __forceinline__ int bwd_first_q_tile(int k0, int Nq, int Nk, int caus
   return qmin <= 0 ? 0 : qmin / 128;
 }
 
+// Last query block that sees a key of the 128-key tile at k0 through the window, or as a sink.
+__device__ __forceinline__ int bwd_last_q_tile(int k0, int Nq, int Nk, int window, int sinks) {
+  const int last = (Nq + 127) / 128 - 1;
+  if (k0 < sinks) return last;
+  const int qmax = k0 + 127 - (Nk - Nq) + window - 1;
+  return qmax < 0 ? -1 : min(last, qmax / 128);
+}
+
+// Window backward: dV, dK of the sink tiles = the sums of their shares' partials, added in share order.
+// One thread per 4 channels of a key.
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_sink_reduce_kernel(const float* __restrict__ part,
+                                                                 __nv_bfloat16* __restrict__ dk,
+                                                                 __nv_bfloat16* __restrict__ dv, int BH, int Nk, int ns,
+                                                                 int parts) {
+  const long long i = blockIdx.x * 256ll + threadIdx.x;
+  const int c = (int)(i % (D / 4)) * 4;
+  const int r = (int)(i / (D / 4) % 128);
+  const int which = (int)(i / (D / 4 * 128) % 2);
+  const long long tile = i / (D / 4 * 256);  // bh * ns + jt
+  if (tile >= (long long)BH * ns) return;
+  const int key = (int)(tile % ns) * 128 + r;
+  if (key >= Nk) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* src = part + ((tile * parts * 2 + which) * 128 + r) * D + c;
+  for (int s = 0; s < parts; ++s) {
+    const float4 x = *reinterpret_cast<const float4*>(src + (size_t)s * 256 * D);
+    acc.x += x.x;
+    acc.y += x.y;
+    acc.z += x.z;
+    acc.w += x.w;
+  }
+  *reinterpret_cast<uint2*>((which ? dk : dv) + ((tile / ns) * Nk + key) * D + c) =
+      make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+}
+
 template <int D>
 __device__ __forceinline__ void bwd_issue_ss_kmajor(uint32_t tmem_d, uint32_t a_smem, uint32_t b_smem) {
   using T = BwdTraits<D>;
@@ -188,7 +230,10 @@ __device__ __forceinline__ void bwd_issue_ss_kmajor(uint32_t tmem_d, uint32_t a_
 // DQ = false (the deterministic backward): dK and dV only; dQ comes from fa_bwd_dq_kernel.
 // EXT: the forward had an additive bias (p.bias) and dropout (p.drop): P is recomputed with the
 // bias, dV uses the dropped and rescaled weights P o Z, and dS = P o (dP o Z - D).
-template <int D, bool DQ = true, bool EXT = false>
+// WIN: sliding window with sinks, key/value heads shared by p.group query heads.  A CTA owns one key tile
+// of one key/value head and visits, head by head, the query blocks that see it, so dK and dV sum over the
+// sharing heads on chip.
+template <int D, bool DQ = true, bool EXT = false, bool WIN = false>
 __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
     fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -207,15 +252,28 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
   // Blocks run in groups of hgroup heads; inside a group, every key tile of those heads, the
   // heaviest (causal) first.  The group's Q, dO and dQ accumulator then stay in L2 while its
   // blocks sweep them, each block starting at its own query tile.
-  const int grp = blockIdx.x / (p.hgroup * p.nkt);
+  // WIN: the cut sink tiles' shares come before everything else (the longest walks first).
+  const int n_cut = WIN && p.parts > 1 ? p.BH * p.ns * p.parts : 0;
+  const bool cut = WIN && (int)blockIdx.x < n_cut;
+  const int jt0 = WIN && p.parts > 1 ? p.ns : 0;  // first key tile of the uncut blocks
+  const int bid = cut ? (int)blockIdx.x : (int)blockIdx.x - n_cut;
+  const int nkt = p.nkt - jt0;
+  const int grp = bid / (p.hgroup * (nkt > 0 ? nkt : 1));
   const int gsz = min(p.hgroup, p.BH - grp * p.hgroup);
-  const int r_in = blockIdx.x - grp * p.hgroup * p.nkt;
-  const int bh = grp * p.hgroup + r_in % gsz;
-  const int jt = r_in / gsz;
+  const int r_in = bid - grp * p.hgroup * nkt;
+  const int bh = cut ? bid % p.BH : grp * p.hgroup + r_in % gsz;
+  const int share = cut ? bid / p.BH / p.ns : 0;
+  const int jt = cut ? bid / p.BH % p.ns : jt0 + r_in / gsz;
   const int k0 = jt * 128;
   const int nqt = (p.Nq + 127) / 128;
   const int i0 = bwd_first_q_tile(k0, p.Nq, p.Nk, p.causal);
-  const int n_q = max(0, nqt - i0);
+  // WIN: the walk is n_per query blocks of each of the group's heads; this CTA takes n_q of them from it0.
+  const int n_per = WIN ? max(0, bwd_last_q_tile(k0, p.Nq, p.Nk, p.window, p.sinks) + 1 - i0) : max(0, nqt - i0);
+  const int it0 = cut ? share * p.plen : 0;
+  const int n_q = !WIN ? n_per : max(0, min(n_per * p.group, cut ? it0 + p.plen : 0x7fffffff) - it0);
+  // First query row of block `it` of the walk, and its query head.
+  auto q_row = [&](int it) -> int { return (i0 + (WIN ? (it0 + it) % n_per : it)) * 128; };
+  auto q_head = [&](int it) -> int { return WIN ? bh * p.group + (it0 + it) / n_per : bh; };
 
   if (threadIdx.x == 0) {
     mbar_init(bar(T::BAR_KV), 1);
@@ -291,7 +349,7 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
     };
     bool ok = true;
     for (int it = 0; it < n_q; ++it) {
-      const int q0 = (i0 + it) * 128;
+      const int q0 = q_row(it);
       [[maybe_unused]] uint32_t braw[2][8];
       if constexpr (EXT) {
         if (has_bias) load_bias(q0, 0, braw[0]);
@@ -302,7 +360,7 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       {
         const int q = q0 + r;
         const bool in = q < p.Nq;
-        const size_t gi = (size_t)bh * p.Nq + (in ? q : 0);
+        const size_t gi = (size_t)q_head(it) * p.Nq + (in ? q : 0);
         float nlse2 = in ? -p.lse[gi] * kLog2e : -INFINITY;
         // EXT: a row the bias hides entirely has LSE = -inf; keep its weights at 0 (a -inf bias
         // entry plus +inf would be NaN).
@@ -328,7 +386,9 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       tc_fence_after();
       const int cmin = p.causal ? shift - q0 : -1;
       // Masking is needed only where this warp holds a key past Nk or a causally hidden entry.
-      const bool masked = __any_sync(0xffffffffu, !key_ok || cmin > cb);
+      // WIN: nor beyond cmax, unless it is a sink.
+      const int cmax = WIN ? (key < p.sinks ? 0x7fffffff : shift - q0 + p.window - 1) : 0x7fffffff;
+      const bool masked = __any_sync(0xffffffffu, !key_ok || cmin > cb || (WIN && cmax < cb + T::CW - 1));
       const float4* st4 = reinterpret_cast<const float4*>(stat);
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
       [[maybe_unused]] const float2 inv2 = make_float2(kLog2e / p.scale_log2, kLog2e / p.scale_log2);  // 1 / scale
@@ -376,10 +436,10 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
           float2 p01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
           float2 p23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
           if (masked) {
-            p01.x = (key_ok && c >= cmin) ? p01.x : 0.f;
-            p01.y = (key_ok && c + 1 >= cmin) ? p01.y : 0.f;
-            p23.x = (key_ok && c + 2 >= cmin) ? p23.x : 0.f;
-            p23.y = (key_ok && c + 3 >= cmin) ? p23.y : 0.f;
+            p01.x = (key_ok && c >= cmin && (!WIN || c <= cmax)) ? p01.x : 0.f;
+            p01.y = (key_ok && c + 1 >= cmin && (!WIN || c + 1 <= cmax)) ? p01.y : 0.f;
+            p23.x = (key_ok && c + 2 >= cmin && (!WIN || c + 2 <= cmax)) ? p23.x : 0.f;
+            p23.y = (key_ok && c + 3 >= cmin && (!WIN || c + 3 <= cmax)) ? p23.y : 0.f;
           }
           float2 t01, t23;
           [[maybe_unused]] float2 z01, z23;  // EXT: dropout factors (kept: 1 / (1 - p), dropped: 0)
@@ -467,7 +527,15 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
-          if (key_ok) {
+          if (cut) {
+            // A share's part of the sums, fp32, [bh, jt, share, dV / dK, key, channel].
+            float4* dst = reinterpret_cast<float4*>(
+                p.part + (((((size_t)bh * p.ns + jt) * p.parts + share) * 2 + which) * 128 + r) * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(__uint_as_float(v[4 * i]) * mul, __uint_as_float(v[4 * i + 1]) * mul,
+                                   __uint_as_float(v[4 * i + 2]) * mul, __uint_as_float(v[4 * i + 3]) * mul);
+          } else if (key_ok) {
             uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -491,7 +559,7 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
     // the block, where the group decides whether to go on (so that no warp is left at a barrier
     // the others never reach).
     for (int it = 0; it < (DQ ? n_q : 0); ++it) {
-      const int q0 = (i0 + it) * 128;
+      const int q0 = q_row(it), hq = q_head(it);
       ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_DQ_FULL), it & 1, abort_flag));
       if constexpr (T::SEP_DQ) {
         uint32_t v[D];
@@ -523,8 +591,8 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
         asm volatile("bar.sync 2, 128;" ::: "memory");
         if (leader) {
           // Rows past Nq fall outside the tensor map and are not written.
-          tma_reduce_add_3d(&tmDQ, sbase + T::OFF_STG, 0, q0, bh);
-          tma_reduce_add_3d(&tmDQ, sbase + T::OFF_STG + 128 * 128, 32, q0, bh);
+          tma_reduce_add_3d(&tmDQ, sbase + T::OFF_STG, 0, q0, hq);
+          tma_reduce_add_3d(&tmDQ, sbase + T::OFF_STG + 128 * 128, 32, q0, hq);
           bulk_commit_group();
         }
       } else {
@@ -548,8 +616,8 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
         auto reduce_half = [&](int h) {  // after the barrier that follows the half's staging
           if (leader) {
             // Rows past Nq fall outside the tensor map and are not written.
-            tma_reduce_add_3d(&tmDQ, stg, 64 * h, q0, bh);
-            tma_reduce_add_3d(&tmDQ, stg + 128 * 128, 64 * h + 32, q0, bh);
+            tma_reduce_add_3d(&tmDQ, stg, 64 * h, q0, hq);
+            tma_reduce_add_3d(&tmDQ, stg + 128 * 128, 64 * h + 32, q0, hq);
             bulk_commit_group();
             bulk_wait_group_read0();  // the staging buffer is read out
           }
@@ -707,10 +775,10 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
         if (!(ok = mbar_wait(bar(T::BAR_QD_EMPTY + s), ((it / T::NS) & 1) ^ 1, abort_flag))) break;
         mbar_arrive_expect_tx(bar(T::BAR_QD_FULL + s), 2 * T::TILE_BYTES);
         const uint32_t dst = sbase + T::OFF_QD + s * 2 * T::TILE_BYTES;
-        const int q0 = (i0 + it) * 128;
+        const int q0 = q_row(it), hq = q_head(it);
         for (int b = 0; b < T::NBOX; ++b) {
-          tma_load_3d(dst + b * T::BOX_BYTES, &tmQ, bar(T::BAR_QD_FULL + s), 64 * b, q0, bh);
-          tma_load_3d(dst + T::TILE_BYTES + b * T::BOX_BYTES, &tmDO, bar(T::BAR_QD_FULL + s), 64 * b, q0, bh);
+          tma_load_3d(dst + b * T::BOX_BYTES, &tmQ, bar(T::BAR_QD_FULL + s), 64 * b, q0, hq);
+          tma_load_3d(dst + T::TILE_BYTES + b * T::BOX_BYTES, &tmDO, bar(T::BAR_QD_FULL + s), 64 * b, q0, hq);
         }
         issued = it + 1;
         if constexpr (EXT) {

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -108,14 +109,14 @@ bool set_smem(K kernel, int bytes) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return false;
   static std::mutex mu;
-  static const void* done[64][16];
+  static const void* done[64][32];
   static int ndone[64];
   std::lock_guard<std::mutex> lock(mu);
   if (dev < 0 || dev >= 64) return false;
   for (int i = 0; i < ndone[dev]; ++i)
     if (done[dev][i] == reinterpret_cast<const void*>(kernel)) return true;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-  if (ndone[dev] < 16) done[dev][ndone[dev]++] = reinterpret_cast<const void*>(kernel);
+  if (ndone[dev] < 32) done[dev][ndone[dev]++] = reinterpret_cast<const void*>(kernel);
   return true;
 }
 
@@ -195,18 +196,27 @@ fa_status make_ext(ExtArgs* ext, const void* bias, int bias_B, int bias_H, int B
   return FA_OK;
 }
 
-template <int D, bool F8 = false, bool EXT = false>
+// Sliding window of the *_window calls, validated and clamped on the host (window, sinks <= Nk).
+struct WinArgs {
+  int window, sinks, group;
+};
+
+template <int D, bool F8 = false, bool EXT = false, bool WIN = false>
 fa_status launch_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int BH, int Nq, int Nk,
                      float scale, int causal, cudaStream_t stream, const float* descale_q = nullptr,
                      const float* descale_k = nullptr, const float* descale_v = nullptr,
-                     const ExtArgs* ext = nullptr) {
+                     const ExtArgs* ext = nullptr, const WinArgs* win = nullptr) {
   using T = fa::FwdTraits<D, F8, EXT>;
   CUtensorMap mq, mk, mv;
-  if (!make_map_3d(&mq, q, D, Nq, BH, F8) || !make_map_3d(&mk, k, D, Nk, BH, F8) ||
-      !make_map_3d(&mv, v, D, Nk, BH, F8))
+  const int kvBH = win ? BH / win->group : BH;
+  if (!make_map_3d(&mq, q, D, Nq, BH, F8) || !make_map_3d(&mk, k, D, Nk, kvBH, F8) ||
+      !make_map_3d(&mv, v, D, Nk, kvBH, F8))
     return FA_ERR_CUDA;
-  if (!set_smem(fa::fa_fwd_kernel<D, F8, EXT>, T::SMEM_BYTES)) return FA_ERR_CUDA;
+  if (!set_smem(fa::fa_fwd_kernel<D, F8, EXT, WIN>, T::SMEM_BYTES)) return FA_ERR_CUDA;
   fa::FwdParams p;
+  p.window = win ? win->window : 0;
+  p.sinks = win ? win->sinks : 0;
+  p.group = win ? win->group : 1;
   set_ext(p, ext);
   p.descale_q = descale_q;
   p.descale_k = descale_k;
@@ -232,7 +242,7 @@ fa_status launch_fwd(const void* q, const void* k, const void* v, void* o, float
   if (loads_per_cta > (1LL << 30)) return FA_ERR_UNSUPPORTED;
   CUtensorMap mb;
   if (!ext_bias_map(&mb, ext, Nq, Nk)) return FA_ERR_CUDA;
-  fa::fa_fwd_kernel<D, F8, EXT><<<(unsigned)blocks, T::THREADS, T::SMEM_BYTES, stream>>>(mq, mk, mv, mb, p);
+  fa::fa_fwd_kernel<D, F8, EXT, WIN><<<(unsigned)blocks, T::THREADS, T::SMEM_BYTES, stream>>>(mq, mk, mv, mb, p);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -329,6 +339,96 @@ fa_status launch_bwd(const void* q, const void* k, const void* v, const void* o,
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   }
   return FA_OK;
+}
+
+// How the window backward cuts the sink tiles' walks over the query blocks, and the fp32 partials it needs.
+struct WinBwdPlan {
+  int ns, parts, plen;
+  size_t part_bytes;
+};
+
+WinBwdPlan win_bwd_plan(int kvBH, int group, int Nq, int Nk, int d, int window, int sinks) {
+  WinBwdPlan w{(sinks + 127) / 128, 1, 0, 0};
+  const long long nqt = (Nq + 127) / 128, nkt = (Nk + 127) / 128;
+  // Blocks of an ordinary key tile's walk and of a sink tile's; a share is as long as an ordinary walk, or
+  // half of a processor's part of all walks where that is more (148 processors).
+  const long long reg = (long long)group * std::min<long long>(nqt, (window + 126) / 128 + 1);
+  const long long snk = (long long)group * nqt;
+  if (w.ns == 0 || snk <= reg) return w;
+  const long long total = (long long)kvBH * (reg * std::max<long long>(0, nkt - w.ns) + snk * w.ns);
+  const long long plen = std::max<long long>(std::max<long long>(reg, 8), (total + 295) / 296);
+  w.parts = (int)((snk + plen - 1) / plen);
+  w.plen = (int)std::min<long long>(plen, 0x7fffffff);
+  if (w.parts > 1) w.part_bytes = (size_t)kvBH * w.ns * w.parts * 2 * 128 * d * sizeof(float);
+  return w;
+}
+
+template <int D>
+fa_status launch_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                            const float* lse, void* dq, void* dk, void* dv, void* ws, int BH, int Nq, int Nk,
+                            float scale, cudaStream_t stream, const WinArgs& win) {
+  using T = fa::BwdTraits<D>;
+  const long long rows = (long long)BH * Nq;
+  const int kvBH = BH / win.group;
+  float* dvec = static_cast<float*>(ws);
+  float* dq_acc = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)rows * 4));
+  fa::fa_bwd_preprocess_kernel<D><<<(unsigned)((rows + 7) / 8), 256, 0, stream>>>(
+      static_cast<const __nv_bfloat16*>(o), static_cast<const __nv_bfloat16*>(dO), dvec, dq_acc, rows);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (Nk > 0) {
+    CUtensorMap mq, mk, mv, mdo, mdq, mb;
+    if (!make_map_3d(&mq, q, D, Nq, BH) || !make_map_3d(&mk, k, D, Nk, kvBH) || !make_map_3d(&mv, v, D, Nk, kvBH) ||
+        !make_map_3d(&mdo, dO, D, Nq, BH) || !make_map_3d_f32(&mdq, dq_acc, D, Nq, BH) ||
+        !ext_bias_map(&mb, nullptr, Nq, Nk))
+      return FA_ERR_CUDA;
+    if (!set_smem(fa::fa_bwd_main_kernel<D, true, false, true>, T::SMEM_BYTES)) return FA_ERR_CUDA;
+    fa::BwdParams p;
+    set_ext(p, nullptr);
+    p.lse = lse;
+    p.dvec = dvec;
+    p.dq_acc = dq_acc;
+    p.dk = static_cast<__nv_bfloat16*>(dk);
+    p.dv = static_cast<__nv_bfloat16*>(dv);
+    p.Nq = Nq;
+    p.Nk = Nk;
+    p.BH = kvBH;
+    p.nkt = (Nk + 127) / 128;
+    p.scale = scale;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.causal = 1;
+    p.window = win.window;
+    p.sinks = win.sinks;
+    p.group = win.group;
+    const WinBwdPlan plan = win_bwd_plan(kvBH, win.group, Nq, Nk, D, win.window, win.sinks);
+    p.ns = plan.ns;
+    p.parts = plan.parts;
+    p.plen = plan.plen;
+    p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(dq_acc) + align256((size_t)rows * D * 4));
+    // Heads per group as in launch_bwd, with the rows a wave of key tiles touches in place of all of them.
+    const int nkt = p.nkt - (plan.parts > 1 ? plan.ns : 0);
+    {
+      const long long per_head = 8LL * std::min<long long>(Nq, (long long)win.window + 128) * D * win.group;
+      long long g = (32LL << 20) / per_head;
+      const long long fill = nkt > 0 ? (num_sms() + nkt - 1) / nkt : 1;
+      g = std::max<long long>(1, std::max(g, fill));
+      p.hgroup = (int)std::min<long long>(g, kvBH);
+    }
+    const long long blocks = (long long)nkt * kvBH + (plan.parts > 1 ? (long long)kvBH * plan.ns * plan.parts : 0);
+    if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    fa::fa_bwd_main_kernel<D, true, false, true><<<(unsigned)blocks, T::THREADS, T::SMEM_BYTES, stream>>>(
+        mq, mk, mv, mdo, mdq, mb, p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (plan.parts > 1) {
+      const long long n = (long long)kvBH * plan.ns * 256 * (D / 4);
+      fa::fa_bwd_sink_reduce_kernel<D><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p.part, p.dk, p.dv, kvBH, Nk,
+                                                                                       plan.ns, plan.parts);
+      if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    }
+  }
+  const long long n8 = rows * D / 8;
+  fa::fa_bwd_dq_convert_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, stream>>>(
+      dq_acc, static_cast<__nv_bfloat16*>(dq), n8);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 template <int D>
@@ -556,6 +656,81 @@ fa_status fa_bwd_deterministic(const void* q, const void* k, const void* v, cons
                                int H, int Nq, int Nk, int d, float scale, int causal, void* stream) {
   return bwd_entry(q, k, v, o, dO, lse, dq, dk, dv, workspace, ws_bytes, B, H, Nq, Nk, d, scale, causal, stream,
                    true);
+}
+
+// Checks of the head counts and the window; fills `win`, clamped to the keys there are.
+static fa_status make_window(WinArgs* win, int H, int Hkv, int Nk, int window, int sinks) {
+  if (Hkv < 0 || window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (H > 0 && (Hkv == 0 || H % Hkv != 0)) return FA_ERR_INVALID_ARG;
+  win->window = std::max(1, std::min(window, Nk));
+  win->sinks = std::min(sinks, Nk);
+  win->group = H > 0 ? H / Hkv : 1;
+  return FA_OK;
+}
+
+fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hkv,
+                        int Nq, int Nk, int d, int window, int sinks, float scale, void* stream) {
+  fa_status st = check_common(B, H, Nq, Nk, d, scale);
+  if (st != FA_OK) return st;
+  WinArgs win;
+  if ((st = make_window(&win, H, Hkv, Nk, window, sinks)) != FA_OK) return st;
+  const long long BH = (long long)B * H;
+  if (BH == 0 || Nq == 0) return FA_OK;
+  if (!q || !o || !lse || (Nk > 0 && (!k || !v))) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || (Nk > 0 && (!aligned16(k) || !aligned16(v))))
+    return FA_ERR_MISALIGNED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (Nk == 0) {
+    const long long rows = BH * Nq;
+    const long long n = rows * d;
+    if ((n + 255) / 256 > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    fa::fa_fwd_empty_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(static_cast<__nv_bfloat16*>(o), lse, rows,
+                                                                         d);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  }
+  return d == 64 ? launch_fwd<64, false, false, true>(q, k, v, o, lse, (int)BH, Nq, Nk, scale, 1, s, nullptr, nullptr,
+                                                      nullptr, nullptr, &win)
+                 : launch_fwd<128, false, false, true>(q, k, v, o, lse, (int)BH, Nq, Nk, scale, 1, s, nullptr, nullptr,
+                                                       nullptr, nullptr, &win);
+}
+
+size_t fa_bwd_window_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks) {
+  WinArgs win;
+  if (check_common(B, H, Nq, Nk, d, 1.f) != FA_OK || make_window(&win, H, Hkv, Nk, window, sinks) != FA_OK) return 0;
+  const size_t rows = (size_t)B * H * Nq;
+  if (rows == 0) return 0;
+  return align256(rows * 4) + align256(rows * d * 4) +
+         win_bwd_plan(B * Hkv, win.group, Nq, Nk, d, win.window, win.sinks).part_bytes;
+}
+
+fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dO, const float* lse,
+                        void* dq, void* dk, void* dv, void* workspace, size_t ws_bytes, int B, int H, int Hkv, int Nq,
+                        int Nk, int d, int window, int sinks, float scale, void* stream) {
+  fa_status st = check_common(B, H, Nq, Nk, d, scale);
+  if (st != FA_OK) return st;
+  WinArgs win;
+  if ((st = make_window(&win, H, Hkv, Nk, window, sinks)) != FA_OK) return st;
+  const long long BH = (long long)B * H, kvBH = (long long)B * Hkv;
+  const bool has_q = BH > 0 && Nq > 0, has_k = kvBH > 0 && Nk > 0;
+  if ((has_q && (!q || !o || !dO || !lse || !dq)) || (has_k && (!k || !v || !dk || !dv))) return FA_ERR_INVALID_ARG;
+  if ((has_q && (!aligned16(q) || !aligned16(o) || !aligned16(dO) || !aligned16(lse) || !aligned16(dq))) ||
+      (has_k && (!aligned16(k) || !aligned16(v) || !aligned16(dk) || !aligned16(dv))))
+    return FA_ERR_MISALIGNED;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!has_q) {
+    // No query: nothing touches any key (nothing but dK and dV is written, and nothing is read).
+    const size_t bytes = (size_t)kvBH * Nk * d * sizeof(__nv_bfloat16);
+    if (has_k && (cudaMemsetAsync(dk, 0, bytes, s) != cudaSuccess || cudaMemsetAsync(dv, 0, bytes, s) != cudaSuccess))
+      return FA_ERR_CUDA;
+    return FA_OK;
+  }
+  const long long rows = BH * Nq;
+  if ((rows * d / 8 + 255) / 256 > 0x7fffffffLL || (rows + 7) / 8 > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const size_t need = fa_bwd_window_workspace_size(B, H, Hkv, Nq, Nk, d, window, sinks);
+  if (!workspace || ws_bytes < need) return FA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return FA_ERR_MISALIGNED;
+  return d == 64 ? launch_bwd_window<64>(q, k, v, o, dO, lse, dq, dk, dv, workspace, (int)BH, Nq, Nk, scale, s, win)
+                 : launch_bwd_window<128>(q, k, v, o, dO, lse, dq, dk, dv, workspace, (int)BH, Nq, Nk, scale, s, win);
 }
 
 size_t fa_decode_workspace_size(int B, int H, int Lmax, int d, int num_splits) {

@@ -110,14 +110,28 @@ struct FwdParams {
   int bias_pb, bias_ph;
   int H;
   DropoutCfg drop;
+  // Sliding-window instantiation only: key j is visible to a query at position p iff j <= p and
+  // (j > p - window or j < sinks); query head bh reads key/value head bh / group.
+  int window, sinks, group;
 };
 
 // One work item: the query unit of rows [q0, q0 + 128 tiles) of (batch, head) bh.  n0 / n1: key tiles
 // query tile 0 / 1 must visit (under the causal mask the last key tile of the unit is hidden from
 // tile 0 entirely, so tile 0 skips it); n_kv = max(n0, n1) K/V tiles are streamed.
+// The window instantiation streams a list of key tiles: the sink tiles 0 .. s - 1, then tiles lo, lo + 1,
+// ...; tile 1 skips the list entries [x0, x1), which its window has left behind.  (Elsewhere the list is
+// 0, 1, 2, ... and nothing is skipped.)
 struct FwdItem {
   int bh, q0, n0, n1, n_kv;
+  int s, lo, x0, x1;
 };
+
+// Key tiles [lo, hi] inside the window of query rows [a, b] (positions a + off .. b + off); rows before
+// the first key see none and visit tile 0 fully masked.
+__device__ __forceinline__ void fwd_window_tiles(int a, int b, int off, int window, int& lo, int& hi) {
+  lo = max(0, a + off - window + 1) / 128;
+  hi = max(0, b + off) / 128;
+}
 
 // Number of 128-key tiles the CTA owning query rows [q0, q0 + span) must visit.
 __device__ __forceinline__ int fwd_num_kv_tiles(int q0, int span, int Nq, int Nk, int causal) {
@@ -211,12 +225,15 @@ __device__ __forceinline__ void fwd_apply_bias_smem(float* s, const uint8_t* box
 }
 
 // EXT: the scores get an additive bias (p.bias) and the weights dropout (p.drop) before P V.
-template <int D, bool F8 = false, bool EXT = false>
+// WIN: sliding window with sinks, query heads sharing key/value heads.  A work item visits the key tiles
+// its rows can see and no others, so its cost follows the window, not the sequence.
+template <int D, bool F8 = false, bool EXT = false, bool WIN = false>
 __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmB,
                   const FwdParams p) {
   static_assert(!(F8 && EXT), "bias and dropout are not combined with FP8 operands");
+  static_assert(!(WIN && (F8 || EXT)), "the window is combined with neither FP8 operands nor bias and dropout");
   using T = FwdTraits<D, F8, EXT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -234,6 +251,8 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
   // K/V ring, the Q slots and all barrier phases run on across items.
   const int n_items = p.nunits * p.BH;
   const int G = gridDim.x;
+  // Key tile of entry j of an item's list.
+  auto key_tile = [](const FwdItem& w, int j) -> int { return WIN ? (j < w.s ? j : j - w.s + w.lo) : j; };
   auto item_at = [&](int r) -> int { return r * G + ((r & 1) ? (G - 1 - (int)blockIdx.x) : (int)blockIdx.x); };
   auto decode = [&](int i) -> FwdItem {
     FwdItem w;
@@ -241,6 +260,23 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
     const int rank = i / p.BH;
     const int unit = p.causal ? (p.nunits - 1 - rank) : rank;
     w.q0 = unit * 128 * p.tiles;
+    w.s = w.lo = w.x0 = w.x1 = 0;
+    if constexpr (WIN) {
+      const int off = p.Nk - p.Nq, last = p.Nq - 1;
+      int hi0, lo1, hi1;
+      fwd_window_tiles(w.q0, min(w.q0 + 127, last), off, p.window, w.lo, hi0);
+      lo1 = w.lo;
+      hi1 = hi0;
+      if (two) fwd_window_tiles(min(w.q0 + 128, last), min(w.q0 + 255, last), off, p.window, lo1, hi1);
+      const int ns = (p.sinks + 127) / 128;
+      w.s = min(ns, w.lo);
+      w.n_kv = w.s + hi1 - w.lo + 1;
+      w.n0 = w.s + hi0 - w.lo + 1;
+      w.x0 = w.s + max(ns, w.lo) - w.lo;
+      w.x1 = max(w.x0, w.s + lo1 - w.lo);
+      w.n1 = w.n_kv - (w.x1 - w.x0);
+      return w;
+    }
     w.n0 = fwd_num_kv_tiles(w.q0, 128, p.Nq, p.Nk, p.causal);
     w.n1 = two ? fwd_num_kv_tiles(w.q0 + 128, 128, p.Nq, p.Nk, p.causal) : w.n0;
     w.n_kv = max(w.n0, w.n1);
@@ -318,6 +354,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
       const int n_own = two ? (t ? w.n1 : w.n0) : (w.n_kv + 1 - t) / 2;  // key tiles this group visits
       int kmax = p.Nk - 1;  // last visible key of this row (inclusive)
       if (p.causal) kmax = min(kmax, row + p.Nk - p.Nq);
+      [[maybe_unused]] const int kmin = row + p.Nk - p.Nq - p.window + 1;  // WIN: first key of the window
       float m_run = -INFINITY, l_run = 0.f, lr_run = 0.f;
       float scale_log2 = p.scale_log2;
       if constexpr (F8) scale_log2 *= __ldg(p.descale_q + bh) * __ldg(p.descale_k + bh);
@@ -328,7 +365,11 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
       // EXT with a bias: this group's staged bias tile, one 64-key box per half of the scores.
       const uint8_t* bias_box = smem + T::OFF_BIAS + t * T::BIAS_TILE;
       for (int step = 0; step < n_own; ++step) {
-        const int j = two ? step : 2 * step + t;  // key tile
+        int j = two ? step : 2 * step + t;  // entry of the item's list, then its key tile
+        if constexpr (WIN) {
+          if (two && t == 1 && step >= w.x0) j += w.x1 - w.x0;
+          j = key_tile(w, j);
+        }
         ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_S_FULL + t), (cnt + step) & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
@@ -340,11 +381,14 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         float* s = reinterpret_cast<float*>(sa);
         float* s2 = reinterpret_cast<float*>(sb);
         const int lim = kmax - 128 * j;  // keys [0, lim] of this tile are visible
-        const bool masked = __any_sync(0xffffffffu, lim < 127);
+        // WIN: of those, keys [wlo, lim] and keys below slim.
+        [[maybe_unused]] const int wlo = kmin - 128 * j;
+        [[maybe_unused]] const int slim = p.sinks - 128 * j;
+        const bool masked = __any_sync(0xffffffffu, lim < 127 || (WIN && wlo > 0 && slim < 128));
         if (masked) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
-            if (c > lim) s[c] = -INFINITY;
+            if (c > lim || (WIN && c < wlo && c >= slim)) s[c] = -INFINITY;
         }
         if constexpr (EXT) {
           if (staged_bias) {
@@ -358,7 +402,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         if (masked) {
 #pragma unroll
           for (int c = 0; c < 64; ++c)
-            if (c + 64 > lim) s2[c] = -INFINITY;
+            if (c + 64 > lim || (WIN && c + 64 < wlo && c + 64 >= slim)) s2[c] = -INFINITY;
         }
         if constexpr (EXT) {
           if (staged_bias) {
@@ -648,33 +692,43 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
           cnt1 += n_kv / 2;
         } else {
           // Two tiles, in the order S0 S1 PV0 S0' PV1 S1' ...; query tile 0 skips the key tiles it
-          // cannot see (j >= n0), tile 1 visits all n_kv = n1.
-          int v_prev = -1;
+          // cannot see (j >= n0), tile 1 visits all n_kv (WIN: all but [x0, x1)).
+          int v_prev = -1;  // load index of the V tile of tile 1's pending P V
+          int d1 = 0;       // P V products of tile 1 issued
+          auto flush1 = [&]() -> bool {
+            if (d1 == 0 && !o_free(1)) return false;
+            if (!pv(1, cnt1 + d1, v_prev, d1 > 0)) return false;
+            release(v_prev);
+            ++d1;
+            v_prev = -1;
+            return true;
+          };
           for (int j = 0; ok && j < w.n_kv; ++j) {
             const int ik = L + 2 * j, iv = ik + 1;
+            const bool has1 = !WIN || j < w.x0 || j >= w.x1;
             if (!(ok = kv_wait(ik))) break;
             tc_fence_after();
             if (j < w.n0) {
               fwd_issue_qk<D, F8>(tS[0], q_smem[0], kv_smem(ik));
               mma_commit_w(bar(T::BAR_S_FULL + 0));
             }
-            if (j > 0) {
-              if (j == 1 && !(ok = o_free(1))) break;
-              if (!(ok = pv(1, cnt1 + j - 1, v_prev, j - 1 > 0))) break;
-              release(v_prev);
+            if (v_prev >= 0 && !(ok = flush1())) break;
+            if (has1) {
+              fwd_issue_qk<D, F8>(tS[1], q_smem[1], kv_smem(ik));
+              mma_commit_w(bar(T::BAR_S_FULL + 1));
             }
-            fwd_issue_qk<D, F8>(tS[1], q_smem[1], kv_smem(ik));
-            mma_commit_w(bar(T::BAR_S_FULL + 1));
             release(ik);
             if (!(ok = kv_wait(iv))) break;
             if (j < w.n0) {
               if (j == 0 && !(ok = o_free(0))) break;
               if (!(ok = pv(0, cnt0 + j, iv, j > 0))) break;
             }
-            v_prev = iv;
+            if (has1)
+              v_prev = iv;
+            else
+              release(iv);
           }
-          if (ok && w.n_kv == 1) ok = o_free(1);
-          if (ok && (ok = pv(1, cnt1 + w.n_kv - 1, v_prev, w.n_kv - 1 > 0))) release(v_prev);
+          if (ok && v_prev >= 0) ok = flush1();
           cnt0 += w.n0;
           cnt1 += w.n1;
         }
@@ -712,7 +766,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
           const CUtensorMap* map = (idx & 1) ? &tmV : &tmK;
           for (int b = 0; b < T::NBOX; ++b)
             tma_load_3d(sbase + T::OFF_KV + s * T::TILE_BYTES + b * T::BOX_BYTES, map, bar(T::BAR_KV_FULL + s),
-                        T::BOX_COLS * b, 128 * (idx >> 1), w.bh);
+                        T::BOX_COLS * b, 128 * key_tile(w, idx >> 1), WIN ? w.bh / p.group : w.bh);
           issued = g + 1;
         }
         L += 2 * w.n_kv;

@@ -336,6 +336,59 @@ FA_API fa_status fa_decode_splitkv_noalloc(const void* q, const void* k_cache, c
                                            void* stream);
 
 /*
+ * Single-token form of fa_fwd_window: one query per (batch, head) against a KV cache with ragged lengths.
+ * Sequence b's query sits at position seqlens[b] - 1, the newest key's, and sees the last `window` keys and
+ * the first `sinks`; no other slot of the cache is read.
+ *
+ *   q, o     [B, H, 1, d] bf16;  lse [B, H] fp32 or NULL
+ *   k_cache, v_cache  [B, Hkv, Lmax, d] bf16 (Hkv divides H; head h reads key/value head h / (H / Hkv))
+ *   seqlens  [B] int32 DEVICE array, clamped to [0, Lmax]; a length of 0 gives O = 0, LSE = -inf
+ *   window >= 1 (>= Lmax: the whole cache), sinks >= 0
+ *   num_splits: parts the visible keys of each sequence are cut into (0 = automatic; at most 256)
+ *   workspace: at least fa_decode_window_workspace_size() bytes, 256-byte aligned; 0 bytes and NULL where
+ *            one part serves.  Calls that may overlap need workspaces of their own.
+ * Up to 8 query heads that share a key/value head are served by one pass over its cache; a larger group
+ * takes one pass per 8 heads.  Limits as fa_decode_splitkv.
+ */
+FA_API size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Lmax, int d, int window, int sinks,
+                                              int num_splits);
+FA_API fa_status fa_decode_window(const void* q, const void* k_cache, const void* v_cache, const int* seqlens,
+                                  int Lmax, int window, int sinks, void* o, float* lse, int B, int H, int Hkv,
+                                  int d, float scale, int num_splits, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
+/*
+ * 4-bit KV cache: keys and values quantised as they are written, attended to in that form, and read back.
+ *
+ * The d channels of a row form groups of 32.  A group has step = bf16(max |x| / 7) and 4-bit codes
+ * clamp(round_half_even(x / step), -7, 7) + 8, and stands for step * (code - 8): 4.5 bits per channel.  A
+ * group of zeros reads back as zeros; a group that holds an infinity or NaN reads back as NaN.
+ *   k_codes, v_codes  [B, Hkv, Lmax, d / 2] bytes;  k_steps, v_steps  [B, Hkv, Lmax, d / 32] bf16
+ * Order of the codes in a row: a group's channels are cut into units (8 channels in k_codes, 4 in v_codes);
+ * unit u of group g is stored at unit position u * (d / 32) + g, its first channel in its lowest nibble.
+ *
+ * fa_kv4_write: rows t < lens[b] of k, v [B, Hkv, T, d] bf16 go to positions starts[b] + t of sequence b.
+ * fa_kv4_read:  positions starts[b] + t, t < lens[b], as bf16 rows t of k, v [B, Hkv, T, d].
+ *   starts, lens  [B] int32 DEVICE arrays, or NULL (starts 0; lens T).  Rows t >= lens[b] or T, and positions
+ *   outside [0, Lmax), are neither read nor written: what was there stays.
+ *   0 <= T <= 2^24, 1 <= Lmax <= 2^24.
+ *
+ * fa_decode_kv4: fa_decode_window over such a cache (same workspace query); K and V are the values that
+ * the codes stand for.  A non-finite group in a visible row makes the outputs of its key/value head's
+ * queries non-finite or meaningless; rows that are not visible are not read.
+ */
+FA_API fa_status fa_kv4_write(const void* k, const void* v, void* k_codes, void* k_steps, void* v_codes,
+                              void* v_steps, const int* starts, const int* lens, int B, int Hkv, int T,
+                              int Lmax, int d, void* stream);
+FA_API fa_status fa_kv4_read(const void* k_codes, const void* k_steps, const void* v_codes, const void* v_steps,
+                             void* k, void* v, const int* starts, const int* lens, int B, int Hkv, int T,
+                             int Lmax, int d, void* stream);
+FA_API fa_status fa_decode_kv4(const void* q, const void* k_codes, const void* k_steps, const void* v_codes,
+                               const void* v_steps, const int* seqlens, int Lmax, int window, int sinks, void* o,
+                               float* lse, int B, int H, int Hkv, int d, float scale, int num_splits,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/*
  * Synchronises `stream`, then returns and clears the calling device's status
  * word: FA_OK, or FA_ERR_TIMEOUT if a device-side wait gave up since the last
  * call.  Returns FA_ERR_CUDA if the synchronisation itself failed.

@@ -9,16 +9,18 @@ C-ABI mirrors (same names, torch tensors in place of pointers):
     fa_fwd, fa_bwd, fa_bwd_deterministic, fa_bwd_workspace_size, fa_decode_splitkv, fa_decode_num_splits,
     fa_decode_partials, fa_decode_merge,
     fa_decode_workspace_size, fa_decode_splitkv_noalloc, fa_quantize_fp8, fa_fwd_fp8, fa_fwd_ext,
-    fa_bwd_ext, fa_fwd_window, fa_bwd_window, fa_bwd_window_workspace_size, fa_get_device_error, fa_debug_set_wait_limit, fa_status_string, fa_version
+    fa_bwd_ext, fa_fwd_window, fa_bwd_window, fa_bwd_window_workspace_size, fa_decode_window,
+    fa_decode_window_workspace_size, fa_kv4_write, fa_kv4_read, fa_decode_kv4, fa_get_device_error, fa_debug_set_wait_limit, fa_status_string, fa_version
 Convenience wrappers that allocate outputs:
     attention_forward, attention_backward, decode_splitkv, quantize_fp8, attention_forward_fp8,
-    attention_forward_window, attention_backward_window
+    attention_forward_window, attention_backward_window, decode_window, kv4_cache, kv4_read, decode_kv4
 """
 from __future__ import annotations
 
 import ctypes
 import math
 import os
+from typing import Any, NamedTuple
 
 __all__ = [
     "FAError", "lib", "lib_path",
@@ -30,6 +32,8 @@ __all__ = [
     "attention_forward_fp8",
     "fa_fwd_window", "fa_bwd_window", "fa_bwd_window_workspace_size",
     "attention_forward_window", "attention_backward_window",
+    "fa_decode_window", "fa_decode_window_workspace_size", "decode_window",
+    "KV4Cache", "kv4_cache", "fa_kv4_write", "fa_kv4_read", "kv4_read", "fa_decode_kv4", "decode_kv4",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -94,6 +98,16 @@ def lib() -> ctypes.CDLL:
     L.fa_bwd_window_workspace_size.restype = sz
     L.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, i, i, i, f, vp]
     L.fa_bwd_window.restype = i
+    L.fa_decode_window_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+    L.fa_decode_window_workspace_size.restype = sz
+    L.fa_decode_window.argtypes = [vp, vp, vp, vp, i, i, i, vp, vp, i, i, i, i, f, i, vp, sz, vp]
+    L.fa_decode_window.restype = i
+    L.fa_kv4_write.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
+    L.fa_kv4_write.restype = i
+    L.fa_kv4_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
+    L.fa_kv4_read.restype = i
+    L.fa_decode_kv4.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, vp, vp, i, i, i, i, f, i, vp, sz, vp]
+    L.fa_decode_kv4.restype = i
     L.fa_debug_set_wait_limit.argtypes = [ctypes.c_ulonglong]
     L.fa_debug_set_wait_limit.restype = i
     L.fa_get_device_error.argtypes = [vp]
@@ -466,6 +480,114 @@ def fa_bwd_window(q, k, v, o, dO, lse, dq, dk, dv, workspace, window: int, sinks
                                    _scale(scale, d), _stream_ptr(stream, dev)), "fa_bwd_window")
 
 
+def fa_decode_window_workspace_size(B: int, H: int, Hkv: int, Lmax: int, d: int, window: int, sinks: int = 0,
+                                    num_splits: int = 0) -> int:
+    return int(lib().fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, *_window_args(window, sinks), num_splits))
+
+
+def _decode_query(q, seqlens, o, lse, workspace):
+    """Checks of what both caches' decodes share; returns B, H, d and the device."""
+    import torch
+    B, H, one, d = q.shape
+    if one != 1:
+        raise ValueError("decode takes one query per (batch, head)")
+    dev = q.device
+    _need(q, "q", torch.bfloat16, dev)
+    _need(seqlens, "seqlens", torch.int32, dev, (B,))
+    _need(o, "o", torch.bfloat16, dev, (B, H, 1, d))
+    if lse is not None:
+        _need(lse, "lse", torch.float32, dev, (B, H))
+    _need(workspace, "workspace", torch.uint8, dev)
+    return B, H, d, dev
+
+
+def fa_decode_window(q, k_cache, v_cache, seqlens, window: int, sinks: int, o, lse, workspace, scale=None,
+                     num_splits: int = 0, stream=None) -> None:
+    """One query per (batch, head) against a bf16 cache through a sliding window with sinks (see include/fa.h:
+    fa_decode_window).  q/o [B,H,1,d], caches [B,Hkv,Lmax,d], seqlens int32 [B]."""
+    import torch
+    B, H, d, dev = _decode_query(q, seqlens, o, lse, workspace)
+    Hkv, Lmax = _kv_heads(k_cache, H, B, d)
+    window, sinks = _window_args(window, sinks)
+    _need(k_cache, "k_cache", torch.bfloat16, dev)
+    _need(v_cache, "v_cache", torch.bfloat16, dev, (B, Hkv, Lmax, d))
+    with _on_device(dev):
+        _check(lib().fa_decode_window(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seqlens), Lmax, window, sinks, _ptr(o),
+                                      _ptr(lse), B, H, Hkv, d, _scale(scale, d), int(num_splits), _ptr(workspace),
+                                      workspace.numel(), _stream_ptr(stream, dev)), "fa_decode_window")
+
+
+class KV4Cache(NamedTuple):
+    """The four tensors of a 4-bit KV cache (format: include/fa.h, fa_kv4_write): codes [B,Hkv,Lmax,d/2] uint8
+    and steps [B,Hkv,Lmax,d/32] bf16 of K and V."""
+    k_codes: Any
+    k_steps: Any
+    v_codes: Any
+    v_steps: Any
+
+
+def _kv4_dims(cache, dev):
+    """Checks a KV4Cache and returns B, Hkv, Lmax and d."""
+    import torch
+    if len(cache) != 4 or not isinstance(cache[0], torch.Tensor) or cache[0].dim() != 4:
+        raise ValueError("expected a KV4Cache (k_codes, k_steps, v_codes, v_steps), codes [B, Hkv, Lmax, d / 2]")
+    B, Hkv, Lmax, half = cache[0].shape
+    for t, n in ((cache[0], "k_codes"), (cache[2], "v_codes")):
+        _need(t, n, torch.uint8, dev, (B, Hkv, Lmax, half))
+    for t, n in ((cache[1], "k_steps"), (cache[3], "v_steps")):
+        _need(t, n, torch.bfloat16, dev, (B, Hkv, Lmax, half // 16))
+    return B, Hkv, Lmax, 2 * half
+
+
+def _kv4_rows(cache, k, v, starts, lens):
+    import torch
+    dev = k.device
+    B, Hkv, Lmax, d = _kv4_dims(cache, dev)
+    if k.dim() != 4:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected [{B}, {Hkv}, T, {d}]")
+    T = k.shape[2]
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, n, torch.bfloat16, dev, (B, Hkv, T, d))
+    for t, n in ((starts, "starts"), (lens, "lens")):
+        if t is not None:
+            _need(t, n, torch.int32, dev, (B,))
+    return B, Hkv, T, Lmax, d, dev
+
+
+def fa_kv4_write(k, v, cache, starts=None, lens=None, stream=None) -> None:
+    """Quantise rows t < lens[b] of k, v [B,Hkv,T,d] bf16 into positions starts[b] + t of the 4-bit cache (see
+    include/fa.h: fa_kv4_write).  starts / lens int32 [B] or None (0 / T)."""
+    B, Hkv, T, Lmax, d, dev = _kv4_rows(cache, k, v, starts, lens)
+    with _on_device(dev):
+        _check(lib().fa_kv4_write(_ptr(k), _ptr(v), *map(_ptr, cache), _ptr(starts), _ptr(lens), B, Hkv, T, Lmax, d,
+                                  _stream_ptr(stream, dev)), "fa_kv4_write")
+
+
+def fa_kv4_read(cache, k, v, starts=None, lens=None, stream=None) -> None:
+    """Positions starts[b] + t, t < lens[b], of the 4-bit cache as bf16 rows t of k, v [B,Hkv,T,d] (see include/fa.h:
+    fa_kv4_read); other rows of k and v are left as they were."""
+    B, Hkv, T, Lmax, d, dev = _kv4_rows(cache, k, v, starts, lens)
+    with _on_device(dev):
+        _check(lib().fa_kv4_read(*map(_ptr, cache), _ptr(k), _ptr(v), _ptr(starts), _ptr(lens), B, Hkv, T, Lmax, d,
+                                 _stream_ptr(stream, dev)), "fa_kv4_read")
+
+
+def fa_decode_kv4(q, cache, seqlens, window: int, sinks: int, o, lse, workspace, scale=None, num_splits: int = 0,
+                  stream=None) -> None:
+    """fa_decode_window over a 4-bit cache (see include/fa.h: fa_decode_kv4).  q/o [B,H,1,d], cache a KV4Cache."""
+    B, H, d, dev = _decode_query(q, seqlens, o, lse, workspace)
+    Bc, Hkv, Lmax, dc = _kv4_dims(cache, dev)
+    if (Bc, dc) != (B, d):
+        raise ValueError(f"the cache holds {Bc} sequences of head dim {dc}, q has {B} of {d}")
+    if H % Hkv if Hkv else H:
+        raise ValueError(f"{H} query heads cannot share {Hkv} key/value heads")
+    window, sinks = _window_args(window, sinks)
+    with _on_device(dev):
+        _check(lib().fa_decode_kv4(_ptr(q), *map(_ptr, cache), _ptr(seqlens), Lmax, window, sinks, _ptr(o), _ptr(lse), B, H,
+                                   Hkv, d, _scale(scale, d), int(num_splits), _ptr(workspace), workspace.numel(),
+                                   _stream_ptr(stream, dev)), "fa_decode_kv4")
+
+
 def fa_debug_set_wait_limit(limit_ns: int, device=None) -> None:
     """Test hook (see include/fa.h: fa_debug_set_wait_limit): the limit of every pipeline wait on
     ``device`` (default: current), 0 restoring the default 2 s."""
@@ -571,3 +693,54 @@ def attention_backward_window(q, k, v, o, lse, dO, window: int, sinks: int = 0, 
         workspace = _workspace(fa_bwd_window_workspace_size(B, H, Hkv, Nq, Nk, d, window, sinks), q.device)
     fa_bwd_window(q, k, v, o, dO, lse, dq, dk, dv, workspace, window, sinks, scale, stream)
     return dq, dk, dv
+
+
+def decode_window(q, k_cache, v_cache, seqlens, window: int, sinks: int = 0, scale=None, num_splits: int = 0, stream=None,
+                  workspace=None):
+    """Allocate O, LSE (and the workspace unless given) and run fa_decode_window; returns (o, lse)."""
+    import torch
+    B, H, _, d = q.shape
+    Hkv, Lmax = _kv_heads(k_cache, H, B, d)
+    o = torch.empty((B, H, 1, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = _workspace(fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks, num_splits), q.device)
+    fa_decode_window(q, k_cache, v_cache, seqlens, window, sinks, o, lse, workspace, scale, num_splits, stream)
+    return o, lse
+
+
+def kv4_cache(B: int, Hkv: int, Lmax: int, d: int, device) -> KV4Cache:
+    """An empty 4-bit cache (its rows read back as zeros until they are written)."""
+    import torch
+    if d not in (64, 128):
+        raise ValueError(f"head dim {d} is not supported")
+    parts = [torch.zeros((B, Hkv, Lmax, n), dtype=t, device=device)
+             for n, t in ((d // 2, torch.uint8), (d // 32, torch.bfloat16))]
+    return KV4Cache(*parts, *(torch.zeros_like(t) for t in parts))
+
+
+def kv4_read(cache, T: int, starts=None, stream=None):
+    """Allocate k, v [B, Hkv, T, d] bf16 and run fa_kv4_read on the T rows from starts[b] (0 when None); rows past
+    the cache's end are zeros."""
+    import torch
+    B, Hkv, _, half = cache[0].shape
+    k = torch.zeros((B, Hkv, T, 2 * half), dtype=torch.bfloat16, device=cache[0].device)
+    v = torch.zeros_like(k)
+    fa_kv4_read(cache, k, v, starts, None, stream)
+    return k, v
+
+
+def decode_kv4(q, cache, seqlens, window=None, sinks: int = 0, scale=None, num_splits: int = 0, stream=None,
+               workspace=None):
+    """Allocate O, LSE (and the workspace unless given) and run fa_decode_kv4 (window None: the whole cache);
+    returns (o, lse)."""
+    import torch
+    B, H, _, d = q.shape
+    _, Hkv, Lmax, _ = cache[0].shape
+    window = max(1, Lmax) if window is None else window
+    o = torch.empty((B, H, 1, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = _workspace(fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks, num_splits), q.device)
+    fa_decode_kv4(q, cache, seqlens, window, sinks, o, lse, workspace, scale, num_splits, stream)
+    return o, lse

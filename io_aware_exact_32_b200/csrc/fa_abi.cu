@@ -13,7 +13,9 @@
 #include "bwd_dq_sm100.cuh"
 #include "bwd_sm100.cuh"
 #include "decode_sm100.cuh"
+#include "decode_window_sm100.cuh"
 #include "fwd_sm100.cuh"
+#include "kv4_sm100.cuh"
 #include "quant_sm100.cuh"
 
 namespace {
@@ -481,6 +483,46 @@ fa_status launch_decode_partials(const void* q, const void* kc, const void* vc, 
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+// Parts a sequence's visible keys are cut into: num_splits, or (0) enough for two waves of CTAs (four to a
+// processor, 148 processors), each with at least one step of 64 keys.  A function of the arguments alone, so
+// the workspace query and the call agree.
+int decode_window_splits(int B, int H, int Hkv, int Lmax, int window, int sinks, int num_splits) {
+  if (num_splits > 0) return std::min(num_splits, kMaxSplits);
+  const long long keys = std::min<long long>(Lmax, (long long)window + sinks);
+  const long long units = (long long)B * Hkv * ((H / Hkv + 7) / 8);
+  const long long want = std::max<long long>(1, 2 * 592 / units);
+  return (int)std::max<long long>(1, std::min<long long>(std::min<long long>(want, kMaxSplits),
+                                                         (keys + fa::kDwStep - 1) / fa::kDwStep));
+}
+
+// Host checks shared by the two caches' decodes (everything but the pointers).
+fa_status check_decode_window(int B, int H, int Hkv, int Lmax, int d, int window, int sinks, float scale,
+                                     int num_splits) {
+  if (B < 0 || H < 0 || Hkv < 0 || num_splits < 0 || window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (H > 0 && (Hkv == 0 || H % Hkv != 0)) return FA_ERR_INVALID_ARG;
+  if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (Lmax < 1 || Lmax > kMaxSeq) return Lmax < 1 ? FA_ERR_INVALID_ARG : FA_ERR_UNSUPPORTED;
+  if (num_splits > kMaxSplits) return FA_ERR_UNSUPPORTED;
+  if ((long long)B * H > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+template <int D, bool Q4>
+fa_status launch_decode_window(fa::DecWinParams p, int B, int H, void* ws, cudaStream_t s) {
+  const long long BH = (long long)B * H;
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)BH * p.S * D * 4));
+  const long long blocks = (long long)B * p.Hkv * p.hblocks * p.S;
+  if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  fa::fa_decode_window_kernel<D, Q4><<<(unsigned)blocks, 32 * fa::kDwWarps, 0, s>>>(p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  if (p.S > 1)
+    fa::fa_decode_merge_kernel<D><<<(unsigned)((BH + 3) / 4), 128, 0, s>>>(p.part_o, p.part_ml, p.o, p.lse, (int)BH,
+                                                                           p.S);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -808,6 +850,132 @@ fa_status fa_decode_merge(const float* part_o, const float* part_ml, int R, int 
   else
     fa::fa_decode_merge_kernel<128><<<grid, 128, 0, s>>>(part_o, part_ml, static_cast<__nv_bfloat16*>(o), lse,
                                                          (int)BH, S, R);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+static fa_status decode_window_entry(const void* q, const void* k, const void* v, const void* k_steps,
+                                     const void* v_steps, const int* seqlens, int Lmax, int window, int sinks, void* o,
+                                     float* lse, int B, int H, int Hkv, int d, float scale, int num_splits,
+                                     void* workspace, size_t ws_bytes, void* stream, bool q4) {
+  const fa_status st = check_decode_window(B, H, Hkv, Lmax, d, window, sinks, scale, num_splits);
+  if (st != FA_OK) return st;
+  if (B == 0 || H == 0) return FA_OK;
+  if (!q || !k || !v || !seqlens || !o || (q4 && (!k_steps || !v_steps))) return FA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || (lse && !aligned16(lse)) ||
+      (q4 && (!aligned16(k_steps) || !aligned16(v_steps))) || (reinterpret_cast<uintptr_t>(seqlens) & 3u))
+    return FA_ERR_MISALIGNED;
+  const size_t need = fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks, num_splits);
+  if (need > 0 && (!workspace || ws_bytes < need)) return FA_ERR_WORKSPACE;
+  if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return FA_ERR_MISALIGNED;
+  fa::DecWinParams p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = k;
+  p.v = v;
+  p.k_steps = static_cast<const __nv_bfloat16*>(k_steps);
+  p.v_steps = static_cast<const __nv_bfloat16*>(v_steps);
+  p.seqlens = seqlens;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.Lmax = Lmax;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.group = H / Hkv;
+  p.hblocks = (p.group + 7) / 8;
+  p.S = decode_window_splits(B, H, Hkv, Lmax, window, sinks, num_splits);
+  p.window = window;
+  p.sinks = sinks;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (q4)
+    return d == 64 ? launch_decode_window<64, true>(p, B, H, workspace, s)
+                   : launch_decode_window<128, true>(p, B, H, workspace, s);
+  return d == 64 ? launch_decode_window<64, false>(p, B, H, workspace, s)
+                 : launch_decode_window<128, false>(p, B, H, workspace, s);
+}
+
+size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Lmax, int d, int window, int sinks,
+                                       int num_splits) {
+  if (check_decode_window(B, H, Hkv, Lmax, d, window, sinks, 1.f, num_splits) != FA_OK || B == 0 || H == 0) return 0;
+  const int S = decode_window_splits(B, H, Hkv, Lmax, window, sinks, num_splits);
+  if (S == 1) return 0;
+  const size_t units = (size_t)B * H * S;
+  return align256(units * d * 4) + align256(units * 2 * 4);
+}
+
+fa_status fa_decode_window(const void* q, const void* k_cache, const void* v_cache, const int* seqlens, int Lmax,
+                           int window, int sinks, void* o, float* lse, int B, int H, int Hkv, int d, float scale,
+                           int num_splits, void* workspace, size_t ws_bytes, void* stream) {
+  return decode_window_entry(q, k_cache, v_cache, nullptr, nullptr, seqlens, Lmax, window, sinks, o, lse, B, H, Hkv, d,
+                             scale, num_splits, workspace, ws_bytes, stream, false);
+}
+
+fa_status fa_decode_kv4(const void* q, const void* k_codes, const void* k_steps, const void* v_codes,
+                        const void* v_steps, const int* seqlens, int Lmax, int window, int sinks, void* o, float* lse,
+                        int B, int H, int Hkv, int d, float scale, int num_splits, void* workspace, size_t ws_bytes,
+                        void* stream) {
+  return decode_window_entry(q, k_codes, v_codes, k_steps, v_steps, seqlens, Lmax, window, sinks, o, lse, B, H, Hkv, d,
+                             scale, num_splits, workspace, ws_bytes, stream, true);
+}
+
+// Checks and parameters shared by the 4-bit cache's write and read; rows == 0 on return: nothing to do.
+static fa_status make_kv4(fa::Kv4RowsParams* p, const void* a, const void* b, const void* k_codes, const void* k_steps,
+                          const void* v_codes, const void* v_steps, const int* starts, const int* lens, int B, int Hkv,
+                          int T, int Lmax, int d) {
+  p->rows = 0;
+  if (B < 0 || Hkv < 0 || T < 0) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (Lmax < 1 || Lmax > kMaxSeq || T > kMaxSeq) return Lmax < 1 ? FA_ERR_INVALID_ARG : FA_ERR_UNSUPPORTED;
+  if ((long long)B * Hkv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  const long long rows = (long long)B * Hkv * T;
+  if (rows == 0) return FA_OK;
+  if (!a || !b || !k_codes || !k_steps || !v_codes || !v_steps) return FA_ERR_INVALID_ARG;
+  if (!aligned16(a) || !aligned16(b) || !aligned16(k_codes) || !aligned16(k_steps) || !aligned16(v_codes) ||
+      !aligned16(v_steps) || (reinterpret_cast<uintptr_t>(starts) & 3u) || (reinterpret_cast<uintptr_t>(lens) & 3u))
+    return FA_ERR_MISALIGNED;
+  if ((rows * (d / 8) + 255) / 256 > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  p->codes[0] = static_cast<uint8_t*>(const_cast<void*>(k_codes));
+  p->codes[1] = static_cast<uint8_t*>(const_cast<void*>(v_codes));
+  p->steps[0] = static_cast<__nv_bfloat16*>(const_cast<void*>(k_steps));
+  p->steps[1] = static_cast<__nv_bfloat16*>(const_cast<void*>(v_steps));
+  p->x[0] = static_cast<const __nv_bfloat16*>(a);
+  p->x[1] = static_cast<const __nv_bfloat16*>(b);
+  p->out[0] = static_cast<__nv_bfloat16*>(const_cast<void*>(a));
+  p->out[1] = static_cast<__nv_bfloat16*>(const_cast<void*>(b));
+  p->starts = starts;
+  p->lens = lens;
+  p->rows = rows;
+  p->Hkv = Hkv;
+  p->T = T;
+  p->Lmax = Lmax;
+  return FA_OK;
+}
+
+fa_status fa_kv4_write(const void* k, const void* v, void* k_codes, void* k_steps, void* v_codes, void* v_steps,
+                       const int* starts, const int* lens, int B, int Hkv, int T, int Lmax, int d, void* stream) {
+  fa::Kv4RowsParams p;
+  const fa_status st = make_kv4(&p, k, v, k_codes, k_steps, v_codes, v_steps, starts, lens, B, Hkv, T, Lmax, d);
+  if (st != FA_OK || p.rows == 0) return st;
+  const dim3 grid((unsigned)((p.rows * (d / 8) + 255) / 256), 2);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d == 64)
+    fa::fa_kv4_write_kernel<64><<<grid, 256, 0, s>>>(p);
+  else
+    fa::fa_kv4_write_kernel<128><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_kv4_read(const void* k_codes, const void* k_steps, const void* v_codes, const void* v_steps, void* k,
+                      void* v, const int* starts, const int* lens, int B, int Hkv, int T, int Lmax, int d,
+                      void* stream) {
+  fa::Kv4RowsParams p;
+  const fa_status st = make_kv4(&p, k, v, k_codes, k_steps, v_codes, v_steps, starts, lens, B, Hkv, T, Lmax, d);
+  if (st != FA_OK || p.rows == 0) return st;
+  const dim3 grid((unsigned)((p.rows * (d / 8) + 255) / 256), 2);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (d == 64)
+    fa::fa_kv4_read_kernel<64><<<grid, 256, 0, s>>>(p);
+  else
+    fa::fa_kv4_read_kernel<128><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -344,18 +344,17 @@ FA_API fa_status fa_decode_splitkv_noalloc(const void* q, const void* k_cache, c
  *   k_cache, v_cache  [B, Hkv, Lmax, d] bf16 (Hkv divides H; head h reads key/value head h / (H / Hkv))
  *   seqlens  [B] int32 DEVICE array, clamped to [0, Lmax]; a length of 0 gives O = 0, LSE = -inf
  *   window >= 1 (>= Lmax: the whole cache), sinks >= 0
- *   num_splits: parts the visible keys of each sequence are cut into (0 = automatic; at most 256)
- *   workspace: at least fa_decode_window_workspace_size() bytes, 256-byte aligned; 0 bytes and NULL where
- *            one part serves.  Calls that may overlap need workspaces of their own.
+ *   workspace: at least fa_decode_window_workspace_size() bytes, 256-byte aligned; contents on entry
+ *            ignored.  Calls that may overlap need workspaces of their own.
+ * The visible keys are cut into chunks by the sizes and lengths alone, and merged in a fixed order: the same call
+ * gives the same bits, whatever ran before.
  * Up to 8 query heads that share a key/value head are served by one pass over its cache; a larger group
  * takes one pass per 8 heads.  Limits as fa_decode_splitkv.
  */
-FA_API size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Lmax, int d, int window, int sinks,
-                                              int num_splits);
+FA_API size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Lmax, int d, int window, int sinks);
 FA_API fa_status fa_decode_window(const void* q, const void* k_cache, const void* v_cache, const int* seqlens,
                                   int Lmax, int window, int sinks, void* o, float* lse, int B, int H, int Hkv,
-                                  int d, float scale, int num_splits, void* workspace, size_t ws_bytes,
-                                  void* stream);
+                                  int d, float scale, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * 4-bit KV cache: keys and values quantised as they are written, attended to in that form, and read back.
@@ -385,8 +384,7 @@ FA_API fa_status fa_kv4_read(const void* k_codes, const void* k_steps, const voi
                              int Lmax, int d, void* stream);
 FA_API fa_status fa_decode_kv4(const void* q, const void* k_codes, const void* k_steps, const void* v_codes,
                                const void* v_steps, const int* seqlens, int Lmax, int window, int sinks, void* o,
-                               float* lse, int B, int H, int Hkv, int d, float scale, int num_splits,
-                               void* workspace, size_t ws_bytes, void* stream);
+                               float* lse, int B, int H, int Hkv, int d, float scale, void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Synchronises `stream`, then returns and clears the calling device's status

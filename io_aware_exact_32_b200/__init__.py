@@ -17,6 +17,7 @@ Convenience wrappers that allocate outputs:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -98,15 +99,15 @@ def lib() -> ctypes.CDLL:
     L.fa_bwd_window_workspace_size.restype = sz
     L.fa_bwd_window.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, i, i, i, i, i, i, i, i, f, vp]
     L.fa_bwd_window.restype = i
-    L.fa_decode_window_workspace_size.argtypes = [i, i, i, i, i, i, i, i]
+    L.fa_decode_window_workspace_size.argtypes = [i, i, i, i, i, i, i]
     L.fa_decode_window_workspace_size.restype = sz
-    L.fa_decode_window.argtypes = [vp, vp, vp, vp, i, i, i, vp, vp, i, i, i, i, f, i, vp, sz, vp]
+    L.fa_decode_window.argtypes = [vp, vp, vp, vp, i, i, i, vp, vp, i, i, i, i, f, vp, sz, vp]
     L.fa_decode_window.restype = i
     L.fa_kv4_write.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
     L.fa_kv4_write.restype = i
     L.fa_kv4_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i, i, i, i, i, vp]
     L.fa_kv4_read.restype = i
-    L.fa_decode_kv4.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, vp, vp, i, i, i, i, f, i, vp, sz, vp]
+    L.fa_decode_kv4.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, vp, vp, i, i, i, i, f, vp, sz, vp]
     L.fa_decode_kv4.restype = i
     L.fa_debug_set_wait_limit.argtypes = [ctypes.c_ulonglong]
     L.fa_debug_set_wait_limit.restype = i
@@ -133,6 +134,10 @@ def _stream_ptr(stream, device=None):
     stream of ``device``.  A torch stream that belongs to another device than the tensors is refused."""
     import torch
     if stream is None:
+        # The raw handle, where torch hands it out: a Stream object takes longer to build than the call.
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and device is not None and device.index is not None:
+            return ctypes.c_void_p(raw(device.index))
         stream = torch.cuda.current_stream(device)
     sdev = getattr(stream, "device", None)
     if device is not None and sdev is not None and torch.device(sdev) != torch.device(device):
@@ -145,11 +150,16 @@ def _on_device(device):
     the shared-memory opt-in and its per-device scratch from the current device, and the default
     stream is the current device's, so the tensors' device must be current while it runs."""
     import torch
+    if isinstance(device, torch.device) and device.index is not None and torch.cuda.current_device() == device.index:
+        return _ALREADY_CURRENT
     return torch.cuda.device(device)
 
 
+_ALREADY_CURRENT = contextlib.nullcontext()
+
+
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None
 
 
 def _check(code: int, where: str):
@@ -161,6 +171,9 @@ def _need(t, name, dtype, device, shape=None):
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is dtype and device.type == "cuda" and t.device == device and t.is_contiguous() and \
+            (shape is None or t.shape == shape):
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device.type != "cuda":
@@ -480,9 +493,9 @@ def fa_bwd_window(q, k, v, o, dO, lse, dq, dk, dv, workspace, window: int, sinks
                                    _scale(scale, d), _stream_ptr(stream, dev)), "fa_bwd_window")
 
 
-def fa_decode_window_workspace_size(B: int, H: int, Hkv: int, Lmax: int, d: int, window: int, sinks: int = 0,
-                                    num_splits: int = 0) -> int:
-    return int(lib().fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, *_window_args(window, sinks), num_splits))
+def fa_decode_window_workspace_size(B: int, H: int, Hkv: int, Lmax: int, d: int, window: int,
+                                    sinks: int = 0) -> int:
+    return int(lib().fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, *_window_args(window, sinks)))
 
 
 def _decode_query(q, seqlens, o, lse, workspace):
@@ -502,7 +515,7 @@ def _decode_query(q, seqlens, o, lse, workspace):
 
 
 def fa_decode_window(q, k_cache, v_cache, seqlens, window: int, sinks: int, o, lse, workspace, scale=None,
-                     num_splits: int = 0, stream=None) -> None:
+                     stream=None) -> None:
     """One query per (batch, head) against a bf16 cache through a sliding window with sinks (see include/fa.h:
     fa_decode_window).  q/o [B,H,1,d], caches [B,Hkv,Lmax,d], seqlens int32 [B]."""
     import torch
@@ -513,8 +526,8 @@ def fa_decode_window(q, k_cache, v_cache, seqlens, window: int, sinks: int, o, l
     _need(v_cache, "v_cache", torch.bfloat16, dev, (B, Hkv, Lmax, d))
     with _on_device(dev):
         _check(lib().fa_decode_window(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(seqlens), Lmax, window, sinks, _ptr(o),
-                                      _ptr(lse), B, H, Hkv, d, _scale(scale, d), int(num_splits), _ptr(workspace),
-                                      workspace.numel(), _stream_ptr(stream, dev)), "fa_decode_window")
+                                      _ptr(lse), B, H, Hkv, d, _scale(scale, d), _ptr(workspace), workspace.numel(),
+                                      _stream_ptr(stream, dev)), "fa_decode_window")
 
 
 class KV4Cache(NamedTuple):
@@ -572,7 +585,7 @@ def fa_kv4_read(cache, k, v, starts=None, lens=None, stream=None) -> None:
                                  _stream_ptr(stream, dev)), "fa_kv4_read")
 
 
-def fa_decode_kv4(q, cache, seqlens, window: int, sinks: int, o, lse, workspace, scale=None, num_splits: int = 0,
+def fa_decode_kv4(q, cache, seqlens, window: int, sinks: int, o, lse, workspace, scale=None,
                   stream=None) -> None:
     """fa_decode_window over a 4-bit cache (see include/fa.h: fa_decode_kv4).  q/o [B,H,1,d], cache a KV4Cache."""
     B, H, d, dev = _decode_query(q, seqlens, o, lse, workspace)
@@ -584,7 +597,7 @@ def fa_decode_kv4(q, cache, seqlens, window: int, sinks: int, o, lse, workspace,
     window, sinks = _window_args(window, sinks)
     with _on_device(dev):
         _check(lib().fa_decode_kv4(_ptr(q), *map(_ptr, cache), _ptr(seqlens), Lmax, window, sinks, _ptr(o), _ptr(lse), B, H,
-                                   Hkv, d, _scale(scale, d), int(num_splits), _ptr(workspace), workspace.numel(),
+                                   Hkv, d, _scale(scale, d), _ptr(workspace), workspace.numel(),
                                    _stream_ptr(stream, dev)), "fa_decode_kv4")
 
 
@@ -695,8 +708,7 @@ def attention_backward_window(q, k, v, o, lse, dO, window: int, sinks: int = 0, 
     return dq, dk, dv
 
 
-def decode_window(q, k_cache, v_cache, seqlens, window: int, sinks: int = 0, scale=None, num_splits: int = 0, stream=None,
-                  workspace=None):
+def decode_window(q, k_cache, v_cache, seqlens, window: int, sinks: int = 0, scale=None, stream=None, workspace=None):
     """Allocate O, LSE (and the workspace unless given) and run fa_decode_window; returns (o, lse)."""
     import torch
     B, H, _, d = q.shape
@@ -704,8 +716,8 @@ def decode_window(q, k_cache, v_cache, seqlens, window: int, sinks: int = 0, sca
     o = torch.empty((B, H, 1, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = _workspace(fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks, num_splits), q.device)
-    fa_decode_window(q, k_cache, v_cache, seqlens, window, sinks, o, lse, workspace, scale, num_splits, stream)
+        workspace = _workspace(fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks), q.device)
+    fa_decode_window(q, k_cache, v_cache, seqlens, window, sinks, o, lse, workspace, scale, stream)
     return o, lse
 
 
@@ -730,7 +742,7 @@ def kv4_read(cache, T: int, starts=None, stream=None):
     return k, v
 
 
-def decode_kv4(q, cache, seqlens, window=None, sinks: int = 0, scale=None, num_splits: int = 0, stream=None,
+def decode_kv4(q, cache, seqlens, window=None, sinks: int = 0, scale=None, stream=None,
                workspace=None):
     """Allocate O, LSE (and the workspace unless given) and run fa_decode_kv4 (window None: the whole cache);
     returns (o, lse)."""
@@ -741,6 +753,6 @@ def decode_kv4(q, cache, seqlens, window=None, sinks: int = 0, scale=None, num_s
     o = torch.empty((B, H, 1, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = _workspace(fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks, num_splits), q.device)
-    fa_decode_kv4(q, cache, seqlens, window, sinks, o, lse, workspace, scale, num_splits, stream)
+        workspace = _workspace(fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks), q.device)
+    fa_decode_kv4(q, cache, seqlens, window, sinks, o, lse, workspace, scale, stream)
     return o, lse

@@ -2,9 +2,14 @@
 // cache (format: kv4_sm100.cuh).
 //
 // Sequence b's query sits at position L - 1 and sees the keys [max(0, L - window), L) and [0, sinks).  These
-// are numbered 0 .. n - 1 (the sinks first); the list is cut into S equal parts (multiples of 64 keys), one CTA
-// each, whose (m, l, O~) partials a second kernel merges with the two-block identity of the online softmax.  No
-// other cache row is read.
+// are numbered 0 .. n - 1 (the sinks first); no other cache row is read.  A unit is a sequence's keys under one
+// key/value head and up to 8 of its query heads.  CTAs work on parts of units, and where a unit has several, a second
+// kernel merges their (m, l, O~) partials with the two-block identity of the online softmax:
+//  * bf16 cache: parts of at most 1024 keys, which the hardware deals out (the pass is bound by memory, whose
+//    speed differs from SM to SM);
+//  * 4-bit cache: one wave of CTAs, each with an equal share of the list of all units' steps, whose loads run
+//    ahead across the ends of units (the pass is bound by instructions, and starting and ending a part costs as
+//    much as 500 keys).
 //
 // Bound: HBM (each cache byte serves at most 8 query heads here).  What the 4-bit form costs instead is
 // instructions: at 6.5 TB/s an SM receives 46 codes a clock and issues 128 lane-instructions, so a code
@@ -12,15 +17,19 @@
 //  * both products run on mma.sync m16n8k16 with the cache as the 16-row operand and 8 query heads as the
 //    8 columns (S = K q: rows are keys; O^T = V^T p: rows are channels), so a code is unpacked once for up to 8
 //    heads, and loads go from global memory straight into the operand registers;
-//  * a code is not converted: (word & 0x000f000f) is a pair of fp16 numbers c * 2^-24 (subnormal, exact in
-//    the tensor core), (word & 0x00f000f0) one of c * 2^-20, whose factor 16 goes into q or the output.
-//    5 instructions for 8 codes;
-//  * K steps multiply the fp32 sums of their group; the -8 of (code - 8) is the sums' starting value;
+//  * a K code is not converted: (word & 0x000f000f) is a pair of fp16 numbers c * 2^-24 (subnormal, exact in
+//    the tensor core), (word & 0x00f000f0) one of c * 2^-20, whose factor 16 goes into q: 5 instructions for
+//    8 codes.  The steps multiply the fp32 sums of their group, and the -8 of (code - 8) is the sums'
+//    starting value;
+//  * a V code becomes code - 8 (or 16 times that) by or-ing 1024 and subtracting, 9 instructions for 8: its sums
+//    run over the whole cache, and subnormal codes with the -8 taken off at the end left a bias of 1e-5 of
+//    8 step (the tensor core aligns products by their exponent fields) that is 3e-3 of the output at 65536
+//    keys;
 //  * V steps multiply the weights, p * step in fp16 (11 bits; 2^-11 relative), transposed between the two
-//    products by movmatrix; the -8 is a product of the same rounded weights with a constant row.
-// fp16 range: q is scaled by a power of two per head so that its largest entry is in [2^14, 2^15); the
-// running maximum is that of x + log2(step) (a power-of-two bound of the key's largest V step), so
-// p * step stays below 2^15 whatever the steps.  The stale maximum is kept until a score outgrows it by 2^8.
+//    products by movmatrix.
+// fp16 range: q is scaled by a power of two per head so that its largest entry is in [2^14, 2^15); the weights'
+// base m holds, beside the running maximum, the exponent of the largest V step so far, so p * step stays
+// below 2^14 whatever the steps.  Both are kept until a score outgrows its maximum by 2^8 or a step its bound.
 // The bf16 form is the same with bf16 products; there p = hi + lo in two bf16 terms (16 bits), since its
 // instruction budget is 3.5 times larger.
 #pragma once
@@ -32,8 +41,9 @@
 namespace fa {
 
 constexpr int kDwWarps = 4;
-constexpr int kDwTile = 16;                     // keys per warp tile
-constexpr int kDwStep = kDwWarps * kDwTile;     // keys per CTA step
+constexpr int kDwTile = 16;   // keys per matrix-instruction tile
+constexpr int kDwHeads = 8;   // query heads per pass over a unit's keys
+
 
 struct DecWinParams {
   const __nv_bfloat16* q;         // [B, H, d]
@@ -42,21 +52,37 @@ struct DecWinParams {
   const __nv_bfloat16* k_steps;   // 4-bit cache only
   const __nv_bfloat16* v_steps;
   const int* seqlens;
-  float* part_o;                  // [B * H * S, D] (S > 1)
-  float* part_ml;                 // [B * H * S, 2]
-  __nv_bfloat16* o;               // [B, H, D] (S == 1)
-  float* lse;                     // [B, H] or null (S == 1)
-  int Lmax, H, Hkv, group, hblocks, S;  // hblocks = ceil(group / 8)
+  float* part_o;                  // partials: bf16 [B * H, S, D], 4 bits [2 grid, 8, D]
+  float* part_ml;                 // the same without D, 2
+  __nv_bfloat16* o;               // [B, H, D]
+  float* lse;                     // [B, H] or null
+  int B, Lmax, H, Hkv, group, hblocks;  // hblocks = ceil(group / 8)
+  int S, min_chunk;                  // bf16: parts per unit, at most; keys in a part, at least
+  int grid;                          // 4 bits: CTAs
   int window, sinks;
   float scale_log2;
 };
 
+// What a sequence's query sees.
+struct DwKeys {
+  int n, ns, jump;  // keys; sinks before the window; list entry e >= ns is cache row e + jump
+};
+__device__ __forceinline__ DwKeys dw_keys(const DecWinParams& p, int b) {
+  DwKeys k;
+  const int L = min(max(__ldg(p.seqlens + b), 0), p.Lmax);
+  const int lo = max(0, L - p.window);
+  k.ns = min(p.sinks, lo);
+  k.n = k.ns + L - lo;
+  k.jump = lo - k.ns;
+  return k;
+}
+
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1, float c0, float c1, float c2, float c3) {
+                                              uint32_t b0, uint32_t b1) {
   asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
@@ -64,6 +90,18 @@ __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint3
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// (a & m) | k in one instruction.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t m, uint32_t k) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(m), "r"(k));
+  return d;
+}
+// Differences of fp16 pairs.
+__device__ __forceinline__ uint32_t f16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 // 8 x 8 matrix of 16-bit entries (lane 4 r + c holds entries (r, 2 c) and (r, 2 c + 1)) transposed.
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
@@ -76,9 +114,10 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// N consecutive 32-bit words (N = 1, 2 or a multiple of 4) from a 4 N-byte aligned address (16 at most).
-template <int N>
-__device__ __forceinline__ void ldg_words(uint32_t (&dst)[N], const void* src) {
+// N consecutive 32-bit words (N = 1, 2 or 4) from a 4 N-byte aligned address.
+template <int N, typename Src>
+__device__ __forceinline__ void load_words(uint32_t (&dst)[N], const Src* src) {  // read-only data
+  static_assert(N == 1 || N == 2 || N == 4, "4, 8 or 16 bytes");
   if constexpr (N == 1) {
     dst[0] = __ldg(reinterpret_cast<const uint32_t*>(src));
   } else if constexpr (N == 2) {
@@ -86,7 +125,6 @@ __device__ __forceinline__ void ldg_words(uint32_t (&dst)[N], const void* src) {
     dst[0] = x.x;
     dst[1] = x.y;
   } else {
-    static_assert(N == 4, "16 bytes");
     const uint4 x = __ldg(reinterpret_cast<const uint4*>(src));
     dst[0] = x.x;
     dst[1] = x.y;
@@ -94,61 +132,105 @@ __device__ __forceinline__ void ldg_words(uint32_t (&dst)[N], const void* src) {
     dst[3] = x.w;
   }
 }
+// N consecutive words from shared memory.
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t (&dst)[N], const uint8_t* src) {
+  if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(src);
+    dst[0] = x.x;
+    dst[1] = x.y;
+  } else {
+    static_assert(N == 4, "8 or 16 bytes");
+    const uint4 x = *reinterpret_cast<const uint4*>(src);
+    dst[0] = x.x;
+    dst[1] = x.y;
+    dst[2] = x.z;
+    dst[3] = x.w;
+  }
+}
 
-// A warp's tile of 16 keys in registers.  Lane 4 g + t holds, of the K rows g and g + 8, the t-th quarter, and of
-// the V rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9, the g-th eighth: the operand layout of the two products.
+// A tile of 16 keys.  Lane 4 g + t works on, of the K rows g and g + 8, the t-th quarter, and of the V rows 2 t,
+// 2 t + 1, 2 t + 8, 2 t + 9, the g-th eighth: the operand layout of the two products.  Base: where the lane's parts
+// of a unit's rows g (K, steps) and 2 t (V) lie (a unit's rows span at most 2^32 bytes).  Loads name the tile's
+// first row and `at`, the distance of tile row r from it: r itself, or where a step is cut by the list's jump or end
+// the row of each entry.
+struct DwRows {
+  __device__ __forceinline__ int operator()(int r) const { return r; }
+};
+
+// bf16 rows in registers.
 template <int D, bool Q4>
-struct DwTile;
+struct DwTile {
+  static_assert(!Q4, "bf16 rows");
+  // 168 registers; four CTAs at 128 spill (1.15x).
+  static constexpr int NT = 1, STEP = kDwWarps * kDwTile, CTAS = 3;
+  uint32_t k[2][D / 32][4];       // 16-byte chunks 4 c + t
+  uint32_t v[4][D / 64][4];       // 16-byte chunks 8 c + g
 
-template <int D>
-struct DwTile<D, true> {
-  static constexpr int NG = D / kKv4Group;
-  uint32_t k[2][NG];       // unit t of every group (8 codes each)
-  uint32_t v[4][NG / 2];   // unit g of every group (4 codes each)
-  uint32_t ks[2][NG / 2];  // steps of K rows g, g + 8 (bf16 pairs)
-  uint32_t vs[2][NG / 2];  // steps of V rows g, g + 8
-
-  // row(i): cache row (from the head's first) of list entry i.
-  template <typename Row>
-  __device__ __forceinline__ void load(const DecWinParams& p, size_t head_row, int g, int t, Row row) {
-    const uint8_t* kc = static_cast<const uint8_t*>(p.k);
-    const uint8_t* vc = static_cast<const uint8_t*>(p.v);
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const size_t at = head_row + row(g + 8 * r);
-      ldg_words<NG>(k[r], kc + at * (D / 2) + 4 * NG * t);
-      ldg_words<NG / 2>(ks[r], p.k_steps + at * NG);
-      ldg_words<NG / 2>(vs[r], p.v_steps + at * NG);
+  struct Base {
+    const uint8_t *k, *v;
+    __device__ __forceinline__ void set(const DecWinParams& p, size_t row, int g, int t) {
+      k = static_cast<const uint8_t*>(p.k) + (row + g) * (2 * D) + 16 * t;
+      v = static_cast<const uint8_t*>(p.v) + (row + 2 * t) * (2 * D) + 16 * g;
     }
+  };
+  template <typename At>
+  __device__ __forceinline__ void load_k(const Base& base, uint32_t row, int g, int, At at) {
+    const uint8_t* kc = base.k + row * (2u * D);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const size_t at = head_row + row(2 * t + (r & 1) + 8 * (r >> 1));
-      ldg_words<NG / 2>(v[r], vc + at * (D / 2) + 2 * NG * g);
-    }
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) load_words<4>(k[r][c], kc + (long long)(at(g + 8 * r) - g) * (2 * D) + 64 * c);
+  }
+  template <typename At>
+  __device__ __forceinline__ void load_v(const Base& base, uint32_t row, int, int t, At at) {
+    const uint8_t* vc = base.v + row * (2u * D);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        load_words<4>(v[r][c], vc + (long long)(at(2 * t + (r & 1) + 8 * (r >> 1)) - 2 * t) * (2 * D) + 128 * c);
   }
 };
 
+// Codes and steps.
 template <int D>
-struct DwTile<D, false> {
-  uint32_t k[2][D / 32][4];  // 16-byte chunks 4 c + t
-  uint32_t v[4][D / 64][4];  // 16-byte chunks 8 c + g
+struct DwTile<D, true> {
+  static constexpr int NG = D / kKv4Group;
+  // Two tiles at a time, whose chains of dependent instructions fill each other's gaps.
+  static constexpr int NT = 2, STEP = kDwWarps * kDwTile * NT, CTAS = 3;
+  uint32_t k[2][NG];       // unit t of every group (8 codes each)
+  uint32_t ks[2][NG / 2];  // steps of K rows g, g + 8 (bf16 pairs)
+  uint32_t v[4][NG / 2];   // unit g of every group (4 codes each)
+  uint32_t vs[2][NG / 2];  // steps of V rows g, g + 8
 
-  template <typename Row>
-  __device__ __forceinline__ void load(const DecWinParams& p, size_t head_row, int g, int t, Row row) {
-    const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(p.k);
-    const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(p.v);
+  struct Base {
+    const uint8_t *k, *v, *ks, *vs;
+    __device__ __forceinline__ void set(const DecWinParams& p, size_t row, int g, int t) {
+      k = static_cast<const uint8_t*>(p.k) + (row + g) * (D / 2) + 4 * NG * t;
+      v = static_cast<const uint8_t*>(p.v) + (row + 2 * t) * (D / 2) + 2 * NG * g;
+      ks = reinterpret_cast<const uint8_t*>(p.k_steps + (row + g) * NG);
+      vs = reinterpret_cast<const uint8_t*>(p.v_steps + (row + g) * NG);
+    }
+  };
+  template <typename At>
+  __device__ __forceinline__ void load_k(const Base& base, uint32_t row, int g, int, At at) {
+    const uint8_t *kc = base.k + row * (D / 2), *st = base.ks + row * (2 * NG);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const size_t at = head_row + row(g + 8 * r);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) ldg_words<4>(k[r][c], kc + at * D + 8 * (4 * c + t));
+      const long long d = at(g + 8 * r) - g;
+      load_words<NG>(k[r], kc + d * (D / 2));
+      load_words<NG / 2>(ks[r], st + d * (2 * NG));
     }
+  }
+  template <typename At>
+  __device__ __forceinline__ void load_v(const Base& base, uint32_t row, int g, int t, At at) {
+    const uint8_t *vc = base.v + row * (D / 2), *st = base.vs + row * (2 * NG);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const size_t at = head_row + row(2 * t + (r & 1) + 8 * (r >> 1));
+    for (int r = 0; r < 4; ++r)
+      load_words<NG / 2>(v[r], vc + (long long)(at(2 * t + (r & 1) + 8 * (r >> 1)) - 2 * t) * (D / 2));
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) ldg_words<4>(v[r][c], vc + at * D + 8 * (8 * c + g));
-    }
+    for (int r = 0; r < 2; ++r) load_words<NG / 2>(vs[r], st + (long long)(at(g + 8 * r) - g) * (2 * NG));
   }
 };
 
@@ -160,20 +242,27 @@ struct DwState;
 template <int D>
 struct DwState<D, true> {
   static constexpr int NG = D / kKv4Group;
-  uint32_t qf[NG][4];    // q of head g: fp16 pairs in the order of the unpacked K codes
-  float c0[NG][2];       // -8 * 2^-24 * (sum of the group's q), heads 2 t, 2 t + 1
-  float fx[2];           // what turns step-weighted sums into scores (log2 units)
-  float m[2], l[2];
-  float acc[NG][2][4];   // group, channels 4 g' + {0, 1} / {2, 3}
-  float sum[4];          // row w of the tile: 2^-24 * sum of the rounded weights of group w
+  // The queries' operands, in shared memory, the same for all warps (by lane): q of head g as fp16 pairs in the order
+  // of the unpacked K codes (16 bytes a group), -8 * 2^-24 * (sum of the group's q) of heads 2 t, 2 t + 1 (8 bytes
+  // a group), and what turns their step-weighted sums into scores in log2 units (8 bytes).
+  static constexpr int Q_BYTES = 32 * (NG * 24 + 8);
+  float fx[2];
+  float m[2], l[2];      // weights are 2^(score - m), l their sum
+  float m2[2];           // running maximum (kept while no score is 2^8 above it)
+  float top[2];          // scores up to here (in units of fx) need no new m
+  uint32_t vtop;         // V steps up to here (bf16, twice) need no new m
+  float acc[NG][2][4];   // group, channels 4 g + {0, 1} / {2, 3}; the odd channels times 16
 
-  __device__ __forceinline__ void init(const DecWinParams& p, const __nv_bfloat16* q, bool live, int g, int t) {
+  // By one warp, q being head g's row (live: there is one).
+  static __device__ __forceinline__ void prepare(const DecWinParams& p, const __nv_bfloat16* q, bool live, int g, int t,
+                                                 uint8_t* sm_q) {
+    const int lane = 4 * g + t;
     float x[NG][8];
     float mx = 0.f;
 #pragma unroll
     for (int w = 0; w < NG; ++w) {
       uint32_t raw[4] = {0u, 0u, 0u, 0u};
-      if (live) ldg_words<4>(raw, q + kKv4Group * w + 8 * t);
+      if (live) load_words<4>(raw, q + kKv4Group * w + 8 * t);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         x[w][2 * i] = bf16lo_to_f32(raw[i]);
@@ -186,7 +275,7 @@ struct DwState<D, true> {
     // Power of two that brings the largest |q| to [2^14, 2^15); its exponent is kept inside fp32's normal range.
     const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -100), 126);
     const float up = __uint_as_float((uint32_t)(14 - e + 127) << 23);
-    const float back = p.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23) * 16777216.f;
+    const float back = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(e - 14 + 127) << 23) * 16777216.f, 1e-37f);
 #pragma unroll
     for (int w = 0; w < NG; ++w) {
       float s = 0.f;
@@ -196,41 +285,51 @@ struct DwState<D, true> {
         s += x[w][i];
       }
       // K words unpack to code pairs (0, 4), 16 (1, 5), (2, 6), 16 (3, 7).
-      qf[w][0] = pack_f16x2(x[w][0], x[w][4]);
-      qf[w][1] = pack_f16x2(x[w][1] * 0.0625f, x[w][5] * 0.0625f);
-      qf[w][2] = pack_f16x2(x[w][2], x[w][6]);
-      qf[w][3] = pack_f16x2(x[w][3] * 0.0625f, x[w][7] * 0.0625f);
+      reinterpret_cast<uint4*>(sm_q)[32 * w + lane] =
+          make_uint4(pack_f16x2(x[w][0], x[w][4]), pack_f16x2(x[w][1] * 0.0625f, x[w][5] * 0.0625f),
+                     pack_f16x2(x[w][2], x[w][6]), pack_f16x2(x[w][3] * 0.0625f, x[w][7] * 0.0625f));
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       s *= -8.f / 16777216.f;
+      const float s0 = __shfl_sync(0xffffffffu, s, 8 * t), s1 = __shfl_sync(0xffffffffu, s, 8 * t + 4);
+      reinterpret_cast<float2*>(sm_q + NG * 512)[32 * w + lane] = make_float2(s0, s1);
+    }
+    const float f0 = __shfl_sync(0xffffffffu, back, 8 * t), f1 = __shfl_sync(0xffffffffu, back, 8 * t + 4);
+    reinterpret_cast<float2*>(sm_q + NG * 768)[lane] = make_float2(f0, f1);
+  }
+  // By every warp, once the operands are there.
+  __device__ __forceinline__ void start(const uint8_t* sm_q, int lane) {
+    const float2 f = reinterpret_cast<const float2*>(sm_q + NG * 768)[lane];
+    fx[0] = f.x;
+    fx[1] = f.y;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) c0[w][h] = __shfl_sync(0xffffffffu, s, 4 * (2 * t + h));
+    for (int w = 0; w < NG; ++w)
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[w][b][i] = 0.f;
-    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      fx[h] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + h));
-      m[h] = -INFINITY;
+      m[h] = m2[h] = top[h] = -INFINITY;
       l[h] = 0.f;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sum[i] = 0.f;
+    vtop = ((66u << 7) | 0x7fu) * 0x10001u;
   }
 
-  __device__ __forceinline__ void step(const DwTile<D, true>& x, bool ok0, bool ok1, int g) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+  // Scores of keys g (s[0], s[1]) and g + 8 for heads 2 t and 2 t + 1, in units of fx.
+  __device__ __forceinline__ void scores(const DwTile<D, true>& x, const uint8_t* sm_q, int lane, float (&s)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = 0.f;
 #pragma unroll
     for (int w = 0; w < NG; ++w) {
       const uint32_t a = x.k[0][w], b = x.k[1][w];
-      float d[4];
-      mma_f16_16816(d, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qf[w][0], qf[w][1],
-                    c0[w][0], c0[w][1], c0[w][0], c0[w][1]);
+      uint32_t qf[4];
+      lds_words<4>(qf, sm_q + 16 * (32 * w + lane));
+      const float2 c0 = *reinterpret_cast<const float2*>(sm_q + NG * 512 + 8 * (32 * w + lane));
+      float d[4] = {c0.x, c0.y, c0.x, c0.y};
+      mma_f16_16816(d, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qf[0], qf[1]);
       const uint32_t a8 = a >> 8, b8 = b >> 8;
-      mma_f16_16816(d, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, qf[w][2], qf[w][3],
-                    d[0], d[1], d[2], d[3]);
+      mma_f16_16816(d, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, qf[2], qf[3]);
       const float s0 = (w & 1) ? bf16hi_to_f32(x.ks[0][w / 2]) : bf16lo_to_f32(x.ks[0][w / 2]);
       const float s1 = (w & 1) ? bf16hi_to_f32(x.ks[1][w / 2]) : bf16lo_to_f32(x.ks[1][w / 2]);
       s[0] = fmaf(s0, d[0], s[0]);
@@ -238,29 +337,35 @@ struct DwState<D, true> {
       s[2] = fmaf(s1, d[2], s[2]);
       s[3] = fmaf(s1, d[3], s[3]);
     }
-    // Scores in log2 units; a key past the list has none.  e: log2 of a power of two above the key's V steps
-    // (not below 2^-60, which keeps the sums in range where V is all but zero).
-    float e[2];
+  }
+
+  // Moves the bounds before the weights of N tiles are formed: a score 2^8 above its head's maximum does, or a V
+  // step above theirs (never below 2^-60, which keeps the sums in range where V is all but zero).
+  template <int N>
+  __device__ __forceinline__ void raise(const DwTile<D, true> (&x)[N], const float (&s)[N][4]) {
+    uint32_t mx = 0u;
+    float y[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      uint32_t mx = x.vs[r][0];
-      if constexpr (NG == 4) mx = __vmaxu2(mx, x.vs[r][1]);
-      mx = max(mx & 0xffffu, mx >> 16);
-      e[r] = fmaxf((float)((int)(mx >> 7) - 126), -60.f);
-    }
+    for (int i = 0; i < N; ++i) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      s[h] = ok0 ? s[h] * fx[h] : -INFINITY;
-      s[2 + h] = ok1 ? s[2 + h] * fx[h] : -INFINITY;
+      for (int w = 0; w < NG / 2; ++w) mx = __vmaxu2(mx, __vmaxu2(x[i].vs[0][w], x[i].vs[1][w]));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) y[h] = fmaxf(y[h], fmaxf(s[i][h], s[i][2 + h]));
     }
-    const float y0 = fmaxf(s[0] + e[0], s[2] + e[1]), y1 = fmaxf(s[1] + e[0], s[3] + e[1]);
-    if (__any_sync(0xffffffffu, y0 > m[0] + 14.f || y1 > m[1] + 14.f)) {
-      float y[2] = {y0, y1};
+    const bool up = __vmaxu2(mx, vtop) != vtop;
+    if (__any_sync(0xffffffffu, up || y[0] > top[0] || y[1] > top[1])) {
+      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
+      const uint32_t bits = max(vtop & 0xffffu, mx | 0x7fu);  // the largest bf16 of that exponent
+      vtop = bits | (bits << 16);
+      const float e = (float)((int)(bits >> 7) - 126);  // steps stay below 2^e
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) y[h] = fmaxf(y[h], __shfl_xor_sync(0xffffffffu, y[h], off));
-        const float mn = fmaxf(m[h], y[h] - 6.f);
+        const float mx2 = fmaxf(m2[h], y[h] * fx[h]);
+        m2[h] = mx2;
+        top[h] = (mx2 + 8.f) / fx[h];
+        const float mn = mx2 - 6.f + e;
         const float f = m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - mn);
         m[h] = mn;
         l[h] *= f;
@@ -271,30 +376,30 @@ struct DwState<D, true> {
             acc[w][b][h] *= f;
             acc[w][b][2 + h] *= f;
           }
-        sum[h] *= f;
       }
     }
+  }
+
+  __device__ __forceinline__ void accumulate(const DwTile<D, true>& x, const float (&s)[4]) {
     float pr[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(s[i] - m[i & 1]);
+    for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(fmaf(s[i], fx[i & 1], -m[i & 1]));
     l[0] += pr[0] + pr[2];
     l[1] += pr[1] + pr[3];
+    auto lo4 = [](uint32_t c) { return f16x2_sub(and_or(c, 0x000f000fu, 0x64006400u), 0x64086408u); };  // code - 8
+    auto hi4 = [](uint32_t c) { return f16x2_sub(and_or(c, 0x00f000f0u, 0x64006400u), 0x64806480u); };  // 16 (code - 8)
 #pragma unroll
     for (int w = 0; w < NG; ++w) {
-      float s0 = (w & 1) ? bf16hi_to_f32(x.vs[0][w / 2]) : bf16lo_to_f32(x.vs[0][w / 2]);
-      float s1 = (w & 1) ? bf16hi_to_f32(x.vs[1][w / 2]) : bf16lo_to_f32(x.vs[1][w / 2]);
+      const float s0 = (w & 1) ? bf16hi_to_f32(x.vs[0][w / 2]) : bf16lo_to_f32(x.vs[0][w / 2]);
+      const float s1 = (w & 1) ? bf16hi_to_f32(x.vs[1][w / 2]) : bf16lo_to_f32(x.vs[1][w / 2]);
       const uint32_t b0 = movmatrix_trans(pack_f16x2(pr[0] * s0, pr[1] * s0));
       const uint32_t b1 = movmatrix_trans(pack_f16x2(pr[2] * s1, pr[3] * s1));
       const uint32_t sel = (w & 1) ? 0x7632u : 0x5410u;
       const uint32_t lo = __byte_perm(x.v[0][w / 2], x.v[1][w / 2], sel);
       const uint32_t hi = __byte_perm(x.v[2][w / 2], x.v[3][w / 2], sel);
       const uint32_t lo8 = lo >> 8, hi8 = hi >> 8;
-      mma_f16_16816(acc[w][0], lo & 0x000f000fu, lo & 0x00f000f0u, hi & 0x000f000fu, hi & 0x00f000f0u, b0, b1,
-                    acc[w][0][0], acc[w][0][1], acc[w][0][2], acc[w][0][3]);
-      mma_f16_16816(acc[w][1], lo8 & 0x000f000fu, lo8 & 0x00f000f0u, hi8 & 0x000f000fu, hi8 & 0x00f000f0u, b0, b1,
-                    acc[w][1][0], acc[w][1][1], acc[w][1][2], acc[w][1][3]);
-      const uint32_t one = g == w ? 0x00010001u : 0u;
-      mma_f16_16816(sum, one, 0u, one, 0u, b0, b1, sum[0], sum[1], sum[2], sum[3]);
+      mma_f16_16816(acc[w][0], lo4(lo), hi4(lo), lo4(hi), hi4(hi), b0, b1);
+      mma_f16_16816(acc[w][1], lo4(lo8), hi4(lo8), lo4(hi8), hi4(hi8), b0, b1);
     }
   }
 
@@ -304,15 +409,13 @@ struct DwState<D, true> {
 #pragma unroll
     for (int w = 0; w < NG; ++w)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float off = -8.f * __shfl_sync(0xffffffffu, sum[h], 4 * w + t);
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int ch = kKv4Group * w + 4 * g + 2 * b;
-          put(ch, 2 * t + h, (acc[w][b][h] + off) * 16777216.f);
-          put(ch + 1, 2 * t + h, (acc[w][b][2 + h] * 0.0625f + off) * 16777216.f);
+          put(ch, 2 * t + h, acc[w][b][h]);
+          put(ch + 1, 2 * t + h, acc[w][b][2 + h] * 0.0625f);
         }
-      }
   }
 };
 
@@ -328,7 +431,7 @@ struct DwState<D, false> {
     for (int c = 0; c < D / 32; ++c) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) qf[c][i] = 0u;
-      if (live) ldg_words<4>(qf[c], q + 8 * (4 * c + t));
+      if (live) load_words<4>(qf[c], q + 8 * (4 * c + t));
     }
     fx = p.scale_log2;
 #pragma unroll
@@ -344,21 +447,25 @@ struct DwState<D, false> {
         for (int i = 0; i < 4; ++i) acc[c][j][i] = 0.f;
   }
 
-  __device__ __forceinline__ void step(const DwTile<D, false>& x, bool ok0, bool ok1, int g) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ void scores(const DwTile<D, false>& x, float (&s)[4]) {
+    float a[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of dependent products
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
-      mma_bf16_16816(s, x.k[0][c][0], x.k[1][c][0], x.k[0][c][1], x.k[1][c][1], qf[c][0], qf[c][1]);
-      mma_bf16_16816(s, x.k[0][c][2], x.k[1][c][2], x.k[0][c][3], x.k[1][c][3], qf[c][2], qf[c][3]);
+      mma_bf16_16816(a, x.k[0][c][0], x.k[1][c][0], x.k[0][c][1], x.k[1][c][1], qf[c][0], qf[c][1]);
+      mma_bf16_16816(b, x.k[0][c][2], x.k[1][c][2], x.k[0][c][3], x.k[1][c][3], qf[c][2], qf[c][3]);
     }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      s[h] = ok0 ? s[h] * fx : -INFINITY;
-      s[2 + h] = ok1 ? s[2 + h] * fx : -INFINITY;
-    }
-    const float y0 = fmaxf(s[0], s[2]), y1 = fmaxf(s[1], s[3]);
-    if (__any_sync(0xffffffffu, y0 > m[0] + 8.f || y1 > m[1] + 8.f)) {
-      float y[2] = {y0, y1};
+    for (int i = 0; i < 4; ++i) s[i] = (a[i] + b[i]) * fx;
+  }
+
+  template <int N>
+  __device__ __forceinline__ void raise(const DwTile<D, false> (&)[N], const float (&s)[N][4]) {
+    float y[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) y[h] = fmaxf(y[h], fmaxf(s[i][h], s[i][2 + h]));
+    if (__any_sync(0xffffffffu, y[0] > m[0] + 8.f || y[1] > m[1] + 8.f)) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -376,6 +483,9 @@ struct DwState<D, false> {
           }
       }
     }
+  }
+
+  __device__ __forceinline__ void accumulate(const DwTile<D, false>& x, const float (&s)[4]) {
     float pr[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(s[i] - m[i & 1]);
@@ -412,82 +522,426 @@ struct DwState<D, false> {
   }
 };
 
-template <int D, bool Q4>
-__global__ void __launch_bounds__(32 * kDwWarps) fa_decode_window_kernel(const DecWinParams p) {
-  __shared__ float sm_o[kDwWarps][8][D + 4];
-  __shared__ float sm_ml[kDwWarps][8][2];
+// Where the warps' states meet at the end of a part of a unit.
+template <int D>
+struct DwMeet {
+  float o[kDwWarps][kDwHeads][D + 4];
+  float ml[kDwWarps][kDwHeads][2];
+
+  // The warp's state; l still spread over the lanes' keys.
+  template <typename State>
+  __device__ __forceinline__ void put(State& st, int warp, int g, int t) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) st.l[h] += __shfl_xor_sync(0xffffffffu, st.l[h], off);
+    st.finish(g, t, [&](int ch, int head, float val) { o[warp][head][ch] = val; });
+    if (g == 0)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        ml[warp][2 * t + h][0] = st.m[h];
+        ml[warp][2 * t + h][1] = st.l[h];
+      }
+  }
+  // After a barrier: the CTA's result for heads head0 ..., the outputs themselves if this part was the whole unit (done),
+  // else the partials row(h).
+  template <typename Row>
+  __device__ __forceinline__ void write(const DecWinParams& p, size_t head0, int nh, bool done, Row row) {
+    for (int idx = threadIdx.x; idx < nh * D; idx += 32 * kDwWarps) {
+      const int h = idx / D, ch = idx % D;
+      float mt = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kDwWarps; ++w) mt = fmaxf(mt, ml[w][h][0]);
+      float v = 0.f, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kDwWarps; ++w) {
+        const float lw = ml[w][h][1];
+        if (lw != 0.f) {  // 0: no key (a NaN sum goes on as one)
+          const float f = ex2_approx(ml[w][h][0] - mt);
+          v = fmaf(f, o[w][h][ch], v);
+          l = fmaf(f, lw, l);
+        }
+      }
+      if (done) {
+        p.o[(head0 + h) * D + ch] = __float2bfloat16(v / l);
+        if (ch == 0 && p.lse) p.lse[head0 + h] = (mt + log2f(l)) * 0.6931471805599453f;
+      } else {
+        const size_t part = row(h);
+        p.part_o[part * D + ch] = v;
+        if (ch == 0) {
+          p.part_ml[2 * part] = l != l ? 0.f : mt;
+          p.part_ml[2 * part + 1] = l;
+        }
+      }
+    }
+  }
+};
+
+// Merges `parts` > 1 partials, rows row(0 ...), of one (batch, head) by a CTA of 256 threads: 8 warps take every eighth
+// partial each, a lane D / 32 channels.
+template <int D, typename Row>
+__device__ __forceinline__ void dw_merge(const DecWinParams& p, int parts, Row row) {
+  constexpr int PER = D / 32;
+  __shared__ float sm_o[8][D], sm_ml[8][2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  float m = -INFINITY, l = 0.f, acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  // A warp's partials warp + 8 i, 32 of them a round: their (m, l) one to a lane, then their rows.
+  for (int c = warp; c < parts; c += 256) {
+    const int n = min(32, (parts - 1 - c) / 8 + 1);
+    const float2 x = lane < n ? ml[row(c + 8 * lane)] : make_float2(-INFINITY, 0.f);
+    float mx = x.x;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    mx = fmaxf(m, mx);
+    const float f = ex2_approx(m - mx);  // 0 at first
+    m = mx;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) acc[e] *= f;
+    const float w = ex2_approx(x.x - m);
+    l = fmaf(w, x.y, l);  // this lane's part
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float* src = p.part_o + row(c + 8 * i) * D + lane * PER;
+      if constexpr (PER == 4) {
+        const float4 v = *reinterpret_cast<const float4*>(src);
+        acc[0] = fmaf(wi, v.x, acc[0]);
+        acc[1] = fmaf(wi, v.y, acc[1]);
+        acc[2] = fmaf(wi, v.z, acc[2]);
+        acc[3] = fmaf(wi, v.w, acc[3]);
+      } else {
+        const float2 v = *reinterpret_cast<const float2*>(src);
+        acc[0] = fmaf(wi, v.x, acc[0]);
+        acc[1] = fmaf(wi, v.y, acc[1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll
+  for (int e = 0; e < PER; ++e) sm_o[warp][lane * PER + e] = acc[e];
+  if (lane == 0) {
+    sm_ml[warp][0] = m;
+    sm_ml[warp][1] = l;
+  }
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float mt = -INFINITY, os = 0.f, ls = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) mt = fmaxf(mt, sm_ml[w][0]);
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float f = ex2_approx(sm_ml[w][0] - mt);
+    os = fmaf(f, sm_o[w][threadIdx.x], os);
+    ls = fmaf(f, sm_ml[w][1], ls);
+  }
+  p.o[(size_t)blockIdx.x * D + threadIdx.x] = __float2bfloat16(os / ls);
+  if (p.lse && threadIdx.x == 0) p.lse[blockIdx.x] = (mt + log2f(ls)) * 0.6931471805599453f;
+}
+
+// ---------------------------------------------------------------------------------------------
+// bf16 cache: one part of one unit per CTA.
+// ---------------------------------------------------------------------------------------------
+// Keys per part: an equal S-th of the unit's in whole steps, or the smallest part.
+__device__ __forceinline__ int dw_chunk(const DecWinParams& p, int n) {
+  constexpr int STEP = DwTile<128, false>::STEP;
+  const int even = (int)(((unsigned)n + p.S - 1) / p.S);
+  return max(p.min_chunk, (even + STEP - 1) / STEP * STEP);
+}
+
+template <int D>
+__global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, false>::CTAS)) fa_decode_window_kernel(const DecWinParams p) {
+  using Tile = DwTile<D, false>;
+  constexpr int STEP = Tile::STEP;
+  __shared__ DwMeet<D> meet;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int s_idx = blockIdx.x % p.S;
   int unit = blockIdx.x / p.S;
   const int hb = unit % p.hblocks;
   unit /= p.hblocks;  // b * Hkv + key/value head
-  const int b = unit / p.Hkv;
-  const int h0 = hb * 8;                      // first head of the group's 8
-  const int nh = min(8, p.group - h0);
+  const int h0 = hb * kDwHeads, nh = min(kDwHeads, p.group - h0);
   const size_t head0 = (size_t)unit * p.group + h0;  // b * H + first query head
-
-  const int L = min(max(p.seqlens[b], 0), p.Lmax);
-  const int lo = max(0, L - p.window);  // first key of the window
-  const int ns = min(p.sinks, lo);      // sinks before it
-  const int n = ns + L - lo;
-  const int chunk = ((n + p.S - 1) / p.S + kDwStep - 1) / kDwStep * kDwStep;
+  const DwKeys keys = dw_keys(p, unit / p.Hkv);
+  const int chunk = dw_chunk(p, keys.n);
   const long long begin = (long long)chunk * s_idx;
-  const int i0 = (int)min(begin, (long long)n), i1 = (int)min(begin + chunk, (long long)n);
+  if (begin >= keys.n) {  // nothing of this sequence is left (n = 0: the first part's CTA writes the outputs)
+    if (s_idx == 0)
+      for (int idx = threadIdx.x; idx < nh * D; idx += 32 * kDwWarps) {
+        p.o[head0 * D + idx] = __float2bfloat16(0.f);
+        if (p.lse && idx < nh) p.lse[head0 + idx] = -INFINITY;
+      }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    return;
+  }
+  const int i0 = (int)begin, i1 = min(i0 + chunk, keys.n), ns = keys.ns, jump = keys.jump;
 
-  DwState<D, Q4> st;
+  typename Tile::Base base;
+  base.set(p, (size_t)unit * p.Lmax, g, t);
+  // The warp's tile of the step at list entry i.  A whole step on one side of the jump is consecutive cache rows
+  // (the test is the same for all warps); elsewhere each row is found by itself, entries past the end repeating the
+  // last one (a key the query sees; their weights are 0).
+  const int w0 = warp * kDwTile;
+  auto whole = [&](int i) { return i + STEP <= i1 && (i >= ns || i + STEP <= ns); };
+  auto row0 = [&](int i) -> uint32_t { return i + w0 + (i >= ns ? jump : 0); };
+  auto row_of = [&](int i) {
+    return [=](int r) -> int {
+      const int e = min(i + w0 + r, i1 - 1);
+      return e + (e >= ns ? jump : 0);
+    };
+  };
+  Tile x[1];
+  auto load_k = [&](int i) {
+    if (whole(i)) x[0].load_k(base, row0(i), g, t, DwRows());
+    else x[0].load_k(base, 0, g, t, row_of(i));
+  };
+  auto load_v = [&](int i) {
+    if (whole(i)) x[0].load_v(base, row0(i), g, t, DwRows());
+    else x[0].load_v(base, 0, g, t, row_of(i));
+  };
+  load_k(i0);
+  load_v(i0);
+  DwState<D, false> st;
   st.init(p, p.q + (head0 + min(g, nh - 1)) * D, g < nh, g, t);
-  const size_t head_row = (size_t)unit * p.Lmax;
-  const int jump = lo - ns;
-  for (int i = i0 + warp * kDwTile; i < i1; i += kDwStep) {
-    DwTile<D, Q4> x;
-    // Entries past the end repeat the last one (a key the query sees); their weights are 0.
-    x.load(p, head_row, g, t, [&](int r) -> size_t {
-      const int k = min(i + r, i1 - 1);
-      return (size_t)(k + (k >= ns ? jump : 0));
-    });
-    st.step(x, i + g < i1, i + g + 8 < i1, g);
-  }
-  // The warps' states meet in shared memory.
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) st.l[h] += __shfl_xor_sync(0xffffffffu, st.l[h], off);
-  st.finish(g, t, [&](int ch, int head, float val) { sm_o[warp][head][ch] = val; });
-  if (g == 0)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      sm_ml[warp][2 * t + h][0] = st.m[h];
-      sm_ml[warp][2 * t + h][1] = st.l[h];
+  // K of the next step is on its way from the moment this one's scores are done, V from this one's products on.
+#pragma unroll 1
+  for (int i = i0; i < i1; i += STEP) {
+    float s[1][4];
+    st.scores(x[0], s[0]);
+    const bool more = i + STEP < i1;
+    if (more) load_k(i + STEP);
+    if (i + STEP > i1) {  // scores past the list's end do not count
+      const int e = i + w0 + g;
+      if (e >= i1) s[0][0] = s[0][1] = -INFINITY;
+      if (e + 8 >= i1) s[0][2] = s[0][3] = -INFINITY;
+      if (i + w0 >= i1) break;  // the warp's tile lies past it altogether
     }
+    st.raise(x, s);
+    st.accumulate(x[0], s[0]);
+    if (more) load_v(i + STEP);
+  }
+  // The merge may be launched: it waits for this grid's end before it reads.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  meet.put(st, warp, g, t);
   __syncthreads();
-  for (int idx = threadIdx.x; idx < nh * D; idx += 32 * kDwWarps) {
-    const int h = idx / D, ch = idx % D;
-    float mt = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kDwWarps; ++w) mt = fmaxf(mt, sm_ml[w][h][0]);
-    float o = 0.f, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kDwWarps; ++w) {
-      const float lw = sm_ml[w][h][1];
-      if (lw != 0.f) {  // 0: no key (a NaN sum goes on as one)
-        const float f = ex2_approx(sm_ml[w][h][0] - mt);
-        o = fmaf(f, sm_o[w][h][ch], o);
-        l = fmaf(f, lw, l);
-      }
-    }
-    const size_t head = head0 + h;
-    if (p.S == 1) {
-      p.o[head * D + ch] = __float2bfloat16(l != 0.f ? o / l : 0.f);
-      if (ch == 0 && p.lse) p.lse[head] = l != 0.f ? (mt + log2f(l)) * 0.6931471805599453f : -INFINITY;
-    } else {
-      p.part_o[(head * p.S + s_idx) * D + ch] = o;
-      if (ch == 0) {
-        p.part_ml[2 * (head * p.S + s_idx)] = l != l ? 0.f : mt;
-        p.part_ml[2 * (head * p.S + s_idx) + 1] = l;
-      }
+  meet.write(p, head0, nh, keys.n <= chunk, [&](int h) { return (head0 + h) * p.S + s_idx; });
+}
+
+// One (batch, head) per CTA; launched while the partials' kernel still runs, it waits for that kernel's end.  A head of
+// one part, or without any key, is left alone.
+template <int D>
+__global__ void __launch_bounds__(256) fa_decode_window_merge_kernel(const DecWinParams p) {
+  const int n = dw_keys(p, blockIdx.x / p.H).n, chunk = dw_chunk(p, n);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this grid ends after the partials' does
+  const int parts = (n + chunk - 1) / chunk;
+  if (parts > 1) dw_merge<D>(p, parts, [&](int c) { return (size_t)blockIdx.x * p.S + c; });
+}
+
+// ---------------------------------------------------------------------------------------------
+// 4-bit cache: equal shares of the list of all units' steps.
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ int dw4_steps(int n) {
+  constexpr int STEP = DwTile<128, true>::STEP;
+  return (n + STEP - 1) / STEP;
+}
+// Steps of sequences 0 .. b - 1, of one unit each; by a whole warp.
+__device__ __forceinline__ int dw4_steps_before(const DecWinParams& p, int b, int lane) {
+  int sum = 0;
+  for (int i = lane; i < b; i += 32) sum += dw4_steps(dw_keys(p, i).n);
+  return __reduce_add_sync(0xffffffffu, sum);
+}
+// Steps per CTA when `total` steps (of all units; below 2^31, checked by the host) are shared out.
+__device__ __forceinline__ int dw4_share(const DecWinParams& p, int total) {
+  return max(1, (int)(((long long)total + p.grid - 1) / p.grid));
+}
+
+// A place in the list of steps.
+struct Dw4Place {
+  int b, in_seq, step, steps;  // sequence, its unit (key/value head, head block), the unit's step and steps
+  DwKeys keys;
+
+  __device__ __forceinline__ void set_seq(const DecWinParams& p, int seq) {
+    b = seq;
+    keys = dw_keys(p, b);
+    steps = dw4_steps(keys.n);
+  }
+  // To the next unit that has a step (there is one).
+  __device__ __forceinline__ void next_unit(const DecWinParams& p) {
+    step = 0;
+    if (++in_seq == p.Hkv * p.hblocks) {
+      in_seq = 0;
+      do set_seq(p, b + 1);
+      while (steps == 0);
     }
   }
+};
+
+template <int D>
+__global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, true>::CTAS)) fa_decode_kv4_kernel(const DecWinParams p) {
+  using Tile = DwTile<D, true>;
+  using State = DwState<D, true>;
+  constexpr int NT = Tile::NT, STEP = Tile::STEP;
+  __shared__ DwMeet<D> meet;
+  __shared__ __align__(16) uint8_t sm_q[State::Q_BYTES];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int per_seq = p.Hkv * p.hblocks;  // units of a sequence
+
+  // This CTA's share [begin, end) of the list of steps, and the place where it begins.
+  int mine = lane < p.B ? dw4_steps(dw_keys(p, lane).n) : 0;
+  int sum = mine;
+  for (int i = lane + 32; i < p.B; i += 32) sum += dw4_steps(dw_keys(p, i).n);
+  const int total = __reduce_add_sync(0xffffffffu, sum) * per_seq;
+  const int share = dw4_share(p, total);
+  const int begin = (int)min((long long)share * blockIdx.x, (long long)total);
+  const int end = (int)min((long long)begin + share, (long long)total);
+  if (begin < end) {
+    Dw4Place at;
+    int first = 0;  // steps before the sequence
+    for (int base = 0;; base += 32) {
+      if (base > 0) mine = base + lane < p.B ? dw4_steps(dw_keys(p, base + lane).n) : 0;
+      int incl = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += up;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, first + incl * per_seq > begin);
+      if (past) {  // at the last 32 sequences at the latest: begin < total
+        const int l = __ffs(past) - 1;
+        at.set_seq(p, base + l);
+        first += __shfl_sync(0xffffffffu, incl - mine, l) * per_seq;
+        break;
+      }
+      first += __shfl_sync(0xffffffffu, incl, 31) * per_seq;
+    }
+    at.in_seq = (begin - first) / at.steps;
+    at.step = begin - first - at.in_seq * at.steps;
+
+    // The loads run a step ahead of the work, across the ends of units.  A step's tile rows as in the bf16 kernel.
+    Dw4Place ahead = at;
+    int to_load = end - begin;
+    typename Tile::Base base;
+    auto set_base = [&]() { base.set(p, (size_t)(ahead.b * p.Hkv + ahead.in_seq / p.hblocks) * p.Lmax, g, t); };
+    set_base();
+    const int w0 = warp * (kDwTile * NT);
+    Tile x[NT];
+    auto whole = [&]() {
+      const int i = ahead.step * STEP;
+      return i + STEP <= ahead.keys.n && (i >= ahead.keys.ns || i + STEP <= ahead.keys.ns);
+    };
+    auto row0 = [&]() -> uint32_t {
+      const int i = ahead.step * STEP;
+      return i + w0 + (i >= ahead.keys.ns ? ahead.keys.jump : 0);
+    };
+    auto row_of = [&](int r) -> int {
+      const int e = min(ahead.step * STEP + w0 + r, ahead.keys.n - 1);
+      return e + (e >= ahead.keys.ns ? ahead.keys.jump : 0);
+    };
+    auto load_k = [&]() {
+      if (to_load <= 0) return;
+      if (whole()) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n].load_k(base, row0() + kDwTile * n, g, t, DwRows());
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n].load_k(base, 0, g, t, [&](int r) { return row_of(kDwTile * n + r); });
+      }
+    };
+    auto load_v = [&]() {  // and on to the next step
+      if (to_load <= 0) return;
+      if (whole()) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n].load_v(base, row0() + kDwTile * n, g, t, DwRows());
+      } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[n].load_v(base, 0, g, t, [&](int r) { return row_of(kDwTile * n + r); });
+      }
+      if (--to_load > 0 && ++ahead.step == ahead.steps) {
+        ahead.next_unit(p);
+        set_base();
+      }
+    };
+    load_k();
+    load_v();
+    State st;
+    int seg0 = begin;  // first step of the segment (this CTA's part of a unit)
+#pragma unroll 1
+    for (int j = begin; j < end; ++j) {
+      if (j == seg0) {
+        if (warp == 0) {
+          const int h0 = at.in_seq % p.hblocks * kDwHeads, nh = min(kDwHeads, p.group - h0);
+          const size_t head0 = (size_t)(at.b * p.Hkv + at.in_seq / p.hblocks) * p.group + h0;
+          State::prepare(p, p.q + (head0 + min(g, nh - 1)) * D, g < nh, g, t, sm_q);
+        }
+        __syncthreads();  // also: the last segment's states have been read
+        st.start(sm_q, lane);
+      }
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) st.scores(x[n], sm_q, lane, s[n]);
+      load_k();
+      const int i = at.step * STEP;
+      bool some = true;
+      if (i + STEP > at.keys.n) {  // scores past the list's end do not count
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int e = i + w0 + kDwTile * n + g;
+          if (e >= at.keys.n) s[n][0] = s[n][1] = -INFINITY;
+          if (e + 8 >= at.keys.n) s[n][2] = s[n][3] = -INFINITY;
+        }
+        some = i + w0 < at.keys.n;
+      }
+      if (some) {
+        st.raise(x, s);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) st.accumulate(x[n], s[n]);
+      }
+      load_v();
+      ++at.step;
+      if (at.step < at.steps && j + 1 < end) continue;
+
+      const int h0 = at.in_seq % p.hblocks * kDwHeads, nh = min(kDwHeads, p.group - h0);
+      const size_t head0 = (size_t)(at.b * p.Hkv + at.in_seq / p.hblocks) * p.group + h0;  // b * H + first query head
+      meet.put(st, warp, g, t);
+      __syncthreads();
+      const size_t part = (2 * (size_t)blockIdx.x + (seg0 == begin ? 0 : 1)) * kDwHeads;
+      meet.write(p, head0, nh, j + 1 - seg0 == at.steps, [&](int h) { return part + h; });
+      seg0 = j + 1;
+      if (j + 1 < end) at.next_unit(p);
+    }
+  }
+  // The merge may be launched: it waits for this grid's end before it reads.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// As fa_decode_window_merge_kernel; a head without any key gets O = 0 and LSE = -inf here.
+template <int D>
+__global__ void __launch_bounds__(256) fa_decode_kv4_merge_kernel(const DecWinParams p) {
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.x / p.H, head = blockIdx.x % p.H;
+  const int per_seq = p.Hkv * p.hblocks;
+  const int share = dw4_share(p, dw4_steps_before(p, p.B, lane) * per_seq);
+  const int steps = dw4_steps(dw_keys(p, b).n);
+  const int in_group = head % p.group;
+  const int unit0 =
+      dw4_steps_before(p, b, lane) * per_seq + (head / p.group * p.hblocks + in_group / kDwHeads) * steps;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this grid ends after the partials' does
+  if (steps == 0) {
+    if (threadIdx.x < D) p.o[(size_t)blockIdx.x * D + threadIdx.x] = __float2bfloat16(0.f);
+    if (threadIdx.x == 0 && p.lse) p.lse[blockIdx.x] = -INFINITY;
+    return;
+  }
+  const int c0 = unit0 / share, parts = (unit0 + steps - 1) / share - c0 + 1;
+  // The partial of share c0 + i is in its first slot if the share begins inside the unit, else in its last.
+  if (parts > 1)
+    dw_merge<D>(p, parts, [&](int i) -> size_t {
+      return (2 * (size_t)(c0 + i) + ((long long)(c0 + i) * share < unit0 ? 1 : 0)) * kDwHeads + in_group % kDwHeads;
+    });
 }
 
 }  // namespace fa

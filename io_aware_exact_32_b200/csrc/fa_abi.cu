@@ -483,44 +483,80 @@ fa_status launch_decode_partials(const void* q, const void* kc, const void* vc, 
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-// Parts a sequence's visible keys are cut into: num_splits, or (0) enough for two waves of CTAs (four to a
-// processor, 148 processors), each with at least one step of 64 keys.  A function of the arguments alone, so
-// the workspace query and the call agree.
-int decode_window_splits(int B, int H, int Hkv, int Lmax, int window, int sinks, int num_splits) {
-  if (num_splits > 0) return std::min(num_splits, kMaxSplits);
+// How the windowed decodes cut the work: functions of the arguments alone, so the workspace query and the calls agree.
+// bf16 cache: a unit's parts, sized to give one wave of CTAs at full length, between 128 and 1024 keys each (larger
+// parts leave a tail at the end of a batch, smaller ones pay for starting and merging: 1024 measured best of 512 to
+// 4096 at B32 H32/8 L8192).
+struct DwCut {
+  int S, min_chunk;
+};
+long long decode_window_units(int B, int H, int Hkv) {
+  return (long long)B * Hkv * ((H / Hkv + fa::kDwHeads - 1) / fa::kDwHeads);
+}
+DwCut decode_window_cut(int B, int H, int Hkv, int Lmax, int window, int sinks) {
+  constexpr long long step = fa::DwTile<128, false>::STEP, slots = 148LL * fa::DwTile<128, false>::CTAS;
   const long long keys = std::min<long long>(Lmax, (long long)window + sinks);
-  const long long units = (long long)B * Hkv * ((H / Hkv + 7) / 8);
-  const long long want = std::max<long long>(1, 2 * 592 / units);
-  return (int)std::max<long long>(1, std::min<long long>(std::min<long long>(want, kMaxSplits),
-                                                         (keys + fa::kDwStep - 1) / fa::kDwStep));
+  long long chunk = decode_window_units(B, H, Hkv) * keys / slots + 1;
+  chunk = (std::min<long long>(std::max<long long>(chunk, 128), 1024) + step - 1) / step * step;
+  chunk = std::max(chunk, (keys + kMaxSplits - 1) / kMaxSplits);
+  return DwCut{(int)((keys + chunk - 1) / chunk), 128};
+}
+// 4-bit cache: one wave of CTAs, or one per step where the longest sequences have fewer.
+int decode_kv4_grid(int B, int H, int Hkv, int Lmax, int window, int sinks) {
+  constexpr long long step = fa::DwTile<128, true>::STEP, slots = 148LL * fa::DwTile<128, true>::CTAS;
+  const long long keys = std::min<long long>(Lmax, (long long)window + sinks);
+  return (int)std::min<long long>(slots, decode_window_units(B, H, Hkv) * ((keys + step - 1) / step));
 }
 
 // Host checks shared by the two caches' decodes (everything but the pointers).
-fa_status check_decode_window(int B, int H, int Hkv, int Lmax, int d, int window, int sinks, float scale,
-                                     int num_splits) {
-  if (B < 0 || H < 0 || Hkv < 0 || num_splits < 0 || window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+fa_status check_decode_window(int B, int H, int Hkv, int Lmax, int d, int window, int sinks, float scale) {
+  if (B < 0 || H < 0 || Hkv < 0 || window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
   if (H > 0 && (Hkv == 0 || H % Hkv != 0)) return FA_ERR_INVALID_ARG;
   if (!(std::isfinite(scale) && scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
   if (Lmax < 1 || Lmax > kMaxSeq) return Lmax < 1 ? FA_ERR_INVALID_ARG : FA_ERR_UNSUPPORTED;
-  if (num_splits > kMaxSplits) return FA_ERR_UNSUPPORTED;
   if ((long long)B * H > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  // The 4-bit decode counts the steps of all units in 32 bits.
+  if (H > 0) {
+    constexpr long long step = fa::DwTile<128, true>::STEP;
+    const long long keys = std::min<long long>(Lmax, (long long)window + sinks);
+    if (decode_window_units(B, H, Hkv) * ((keys + step - 1) / step) > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  }
   return FA_OK;
 }
 
 template <int D, bool Q4>
-fa_status launch_decode_window(fa::DecWinParams p, int B, int H, void* ws, cudaStream_t s) {
-  const long long BH = (long long)B * H;
+fa_status launch_decode_window(fa::DecWinParams p, void* ws, cudaStream_t s) {
+  const long long BH = (long long)p.B * p.H;
   p.part_o = static_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float*>(static_cast<char*>(ws) + align256((size_t)BH * p.S * D * 4));
-  const long long blocks = (long long)B * p.Hkv * p.hblocks * p.S;
-  if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-  fa::fa_decode_window_kernel<D, Q4><<<(unsigned)blocks, 32 * fa::kDwWarps, 0, s>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-  if (p.S > 1)
-    fa::fa_decode_merge_kernel<D><<<(unsigned)((BH + 3) / 4), 128, 0, s>>>(p.part_o, p.part_ml, p.o, p.lse, (int)BH,
-                                                                           p.S);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  if constexpr (Q4) {
+    p.grid = decode_kv4_grid(p.B, p.H, p.Hkv, p.Lmax, p.window, p.sinks);
+    p.part_ml = p.part_o + (size_t)2 * p.grid * fa::kDwHeads * D;
+    fa::fa_decode_kv4_kernel<D><<<(unsigned)p.grid, 32 * fa::kDwWarps, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+  } else {
+    const DwCut cut = decode_window_cut(p.B, p.H, p.Hkv, p.Lmax, p.window, p.sinks);
+    p.S = cut.S;
+    p.min_chunk = cut.min_chunk;
+    p.part_ml = p.part_o + (size_t)BH * p.S * D;
+    const long long blocks = (long long)p.B * p.Hkv * p.hblocks * p.S;
+    if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+    fa::fa_decode_window_kernel<D><<<(unsigned)blocks, 32 * fa::kDwWarps, 0, s>>>(p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (p.S == 1) return FA_OK;
+  }
+  // Programmatic dependent launch: the merge's CTAs start while the last of the partials are written.
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)BH);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  void (*merge)(fa::DecWinParams) = Q4 ? fa::fa_decode_kv4_merge_kernel<D> : fa::fa_decode_window_merge_kernel<D>;
+  return cudaLaunchKernelEx(&cfg, merge, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace
@@ -855,16 +891,15 @@ fa_status fa_decode_merge(const float* part_o, const float* part_ml, int R, int 
 
 static fa_status decode_window_entry(const void* q, const void* k, const void* v, const void* k_steps,
                                      const void* v_steps, const int* seqlens, int Lmax, int window, int sinks, void* o,
-                                     float* lse, int B, int H, int Hkv, int d, float scale, int num_splits,
-                                     void* workspace, size_t ws_bytes, void* stream, bool q4) {
-  const fa_status st = check_decode_window(B, H, Hkv, Lmax, d, window, sinks, scale, num_splits);
+                                     float* lse, int B, int H, int Hkv, int d, float scale, void* workspace, size_t ws_bytes, void* stream, bool q4) {
+  const fa_status st = check_decode_window(B, H, Hkv, Lmax, d, window, sinks, scale);
   if (st != FA_OK) return st;
   if (B == 0 || H == 0) return FA_OK;
   if (!q || !k || !v || !seqlens || !o || (q4 && (!k_steps || !v_steps))) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || (lse && !aligned16(lse)) ||
       (q4 && (!aligned16(k_steps) || !aligned16(v_steps))) || (reinterpret_cast<uintptr_t>(seqlens) & 3u))
     return FA_ERR_MISALIGNED;
-  const size_t need = fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks, num_splits);
+  const size_t need = fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks);
   if (need > 0 && (!workspace || ws_bytes < need)) return FA_ERR_WORKSPACE;
   if (need > 0 && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return FA_ERR_MISALIGNED;
   fa::DecWinParams p;
@@ -876,45 +911,43 @@ static fa_status decode_window_entry(const void* q, const void* k, const void* v
   p.seqlens = seqlens;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
+  p.B = B;
   p.Lmax = Lmax;
   p.H = H;
   p.Hkv = Hkv;
   p.group = H / Hkv;
-  p.hblocks = (p.group + 7) / 8;
-  p.S = decode_window_splits(B, H, Hkv, Lmax, window, sinks, num_splits);
+  p.hblocks = (p.group + fa::kDwHeads - 1) / fa::kDwHeads;
   p.window = window;
   p.sinks = sinks;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (q4)
-    return d == 64 ? launch_decode_window<64, true>(p, B, H, workspace, s)
-                   : launch_decode_window<128, true>(p, B, H, workspace, s);
-  return d == 64 ? launch_decode_window<64, false>(p, B, H, workspace, s)
-                 : launch_decode_window<128, false>(p, B, H, workspace, s);
+    return d == 64 ? launch_decode_window<64, true>(p, workspace, s)
+                   : launch_decode_window<128, true>(p, workspace, s);
+  return d == 64 ? launch_decode_window<64, false>(p, workspace, s)
+                 : launch_decode_window<128, false>(p, workspace, s);
 }
 
-size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Lmax, int d, int window, int sinks,
-                                       int num_splits) {
-  if (check_decode_window(B, H, Hkv, Lmax, d, window, sinks, 1.f, num_splits) != FA_OK || B == 0 || H == 0) return 0;
-  const int S = decode_window_splits(B, H, Hkv, Lmax, window, sinks, num_splits);
-  if (S == 1) return 0;
-  const size_t units = (size_t)B * H * S;
-  return align256(units * d * 4) + align256(units * 2 * 4);
+size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Lmax, int d, int window, int sinks) {
+  if (check_decode_window(B, H, Hkv, Lmax, d, window, sinks, 1.f) != FA_OK || B == 0 || H == 0) return 0;
+  const size_t S = decode_window_cut(B, H, Hkv, Lmax, window, sinks).S;
+  const size_t grid = decode_kv4_grid(B, H, Hkv, Lmax, window, sinks);
+  return align256(std::max((size_t)B * H * S, 2 * grid * fa::kDwHeads) * (d + 2) * 4);
 }
 
 fa_status fa_decode_window(const void* q, const void* k_cache, const void* v_cache, const int* seqlens, int Lmax,
                            int window, int sinks, void* o, float* lse, int B, int H, int Hkv, int d, float scale,
-                           int num_splits, void* workspace, size_t ws_bytes, void* stream) {
+                           void* workspace, size_t ws_bytes, void* stream) {
   return decode_window_entry(q, k_cache, v_cache, nullptr, nullptr, seqlens, Lmax, window, sinks, o, lse, B, H, Hkv, d,
-                             scale, num_splits, workspace, ws_bytes, stream, false);
+                             scale, workspace, ws_bytes, stream, false);
 }
 
 fa_status fa_decode_kv4(const void* q, const void* k_codes, const void* k_steps, const void* v_codes,
                         const void* v_steps, const int* seqlens, int Lmax, int window, int sinks, void* o, float* lse,
-                        int B, int H, int Hkv, int d, float scale, int num_splits, void* workspace, size_t ws_bytes,
+                        int B, int H, int Hkv, int d, float scale, void* workspace, size_t ws_bytes,
                         void* stream) {
   return decode_window_entry(q, k_codes, v_codes, k_steps, v_steps, seqlens, Lmax, window, sinks, o, lse, B, H, Hkv, d,
-                             scale, num_splits, workspace, ws_bytes, stream, true);
+                             scale, workspace, ws_bytes, stream, true);
 }
 
 // Checks and parameters shared by the 4-bit cache's write and read; rows == 0 on return: nothing to do.

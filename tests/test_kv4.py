@@ -70,11 +70,11 @@ def L():
 
 
 def dec(L, q4, q=A16, seq=A16, ws=A16, ws_bytes=1 << 30, steps=A16, k=A16, Lmax=4096, window=100, sinks=4, B=2, H=4,
-        Hkv=2, d=128, S=0, scale=0.088):
+        Hkv=2, d=128, scale=0.088):
     if q4:
-        return L.fa_decode_kv4(q, k, steps, A16, A16, seq, Lmax, window, sinks, A16, A16, B, H, Hkv, d, scale, S, ws,
+        return L.fa_decode_kv4(q, k, steps, A16, A16, seq, Lmax, window, sinks, A16, A16, B, H, Hkv, d, scale, ws,
                                ws_bytes, NULL)
-    return L.fa_decode_window(q, k, A16, seq, Lmax, window, sinks, A16, A16, B, H, Hkv, d, scale, S, ws, ws_bytes, NULL)
+    return L.fa_decode_window(q, k, A16, seq, Lmax, window, sinks, A16, A16, B, H, Hkv, d, scale, ws, ws_bytes, NULL)
 
 
 @pytest.mark.parametrize("q4", [False, True])
@@ -86,17 +86,15 @@ def test_decode_refusals(L, q4):
     assert dec(L, q4, sinks=-1) == 1
     assert dec(L, q4, Lmax=0) == 1
     assert dec(L, q4, Lmax=(1 << 24) + 1) == 2
-    assert dec(L, q4, S=257) == 2
-    assert dec(L, q4, S=-1) == 1
     assert dec(L, q4, scale=float("nan")) == 1
     assert dec(L, q4, q=NULL) == 1
     assert dec(L, q4, k=NULL) == 1
     assert dec(L, q4, k=MIS) == 3
     assert dec(L, q4, seq=NULL) == 1
     assert dec(L, q4, seq=ctypes.c_void_p(0x10002)) == 3
-    assert dec(L, q4, ws=NULL, S=2) == 4
-    assert dec(L, q4, ws_bytes=8, S=2) == 4
-    assert dec(L, q4, ws=ctypes.c_void_p(0x10010), S=2) == 3
+    assert dec(L, q4, ws=NULL) == 4
+    assert dec(L, q4, ws_bytes=8) == 4
+    assert dec(L, q4, ws=ctypes.c_void_p(0x10010)) == 3
     assert dec(L, q4, B=0) == 0
     if q4:
         assert dec(L, q4, steps=NULL) == 1
@@ -105,12 +103,15 @@ def test_decode_refusals(L, q4):
 
 def test_decode_workspace(L):
     f = L.fa_decode_window_workspace_size
-    assert f(2, 4, 2, 4096, 128, 100, 4, 1) == 0
-    assert f(2, 4, 2, 4096, 128, 100, 4, 3) == 2 * 4 * 3 * 128 * 4 + 256
-    assert f(2, 4, 2, 4096, 128, 100, 4, 0) == 2 * 4 * 2 * 128 * 4 + 256   # 104 visible keys: two steps of 64
-    assert f(2, 4, 3, 4096, 128, 100, 4, 0) == 0
-    assert f(2, 4, 2, 0, 128, 100, 4, 0) == 0
-    assert f(64, 64, 64, 1 << 24, 128, 1 << 24, 4, 0) == 0                 # as many heads as there is room
+    up = lambda rows: (rows * 130 * 4 + 255) // 256 * 256                    # noqa: E731  d = 128: fp32 O, m, l a row
+    assert f(1, 4, 2, 4096, 128, 64, 0) == up(2 * 2 * 8)                     # 4 bits: a step a head, two slots of 8 rows
+    assert f(1, 40, 1, 4096, 128, 250, 10) == up(2 * 15 * 8)                 # three steps of 128 for each of five blocks of heads
+    assert f(64, 64, 64, 1 << 20, 128, 1 << 24, 4) == up(64 * 64 * 256)      # bf16: no more than 256 parts
+    assert f(2, 4, 3, 4096, 128, 100, 4) == 0
+    assert f(2, 4, 2, 0, 128, 100, 4) == 0
+    assert f(0, 4, 2, 4096, 128, 100, 4) == 0
+    assert f(64, 64, 64, 1 << 24, 128, 1 << 24, 4) > 0
+    assert f(1 << 15, 64, 64, 1 << 24, 128, 1 << 24, 4) == 0                 # 2^38 steps are not counted
 
 
 @pytest.mark.parametrize("name", ["fa_kv4_write", "fa_kv4_read"])
@@ -283,7 +284,7 @@ def _visible_rows(lens, Lmax, window, sinks):
     return torch.from_numpy(m)
 
 
-def _run_decode(q4, case, window, sinks, splits=0):
+def _run_decode(q4, case, window, sinks):
     """Kernel and definition; invisible cache rows are poisoned."""
     q, k, v, lens = case
     scale = 1 / math.sqrt(q.shape[-1])
@@ -299,7 +300,7 @@ def _run_decode(q4, case, window, sinks, splits=0):
             at = hidden[b].to(gc.DEV)
             cache.k_steps[b, :, at] = float("nan")
             cache.v_steps[b, :, at] = float("nan")
-        o, lse = fa.decode_kv4(qd, cache, nd, window, sinks, scale=scale, num_splits=splits)
+        o, lse = fa.decode_kv4(qd, cache, nd, window, sinks, scale=scale)
     else:
         r = OW.decode(_np(q)[:, :, 0], _np(k), _np(v), L, window, sinks, scale)
         # the weights enter as two bf16 terms (2^-17): only the output's own rounding and fp32 remain
@@ -308,7 +309,7 @@ def _run_decode(q4, case, window, sinks, splits=0):
         for b in range(len(L)):
             kp[b, :, hidden[b]] = float("nan")
             vp[b, :, hidden[b]] = float("nan")
-        o, lse = fa.decode_window(qd, kp.to(gc.DEV), vp.to(gc.DEV), nd, window, sinks, scale=scale, num_splits=splits)
+        o, lse = fa.decode_window(qd, kp.to(gc.DEV), vp.to(gc.DEV), nd, window, sinks, scale=scale)
     torch.cuda.synchronize()
     assert fa.fa_get_device_error() == 0
     _within(o[:, :, 0], r["o"], r["o_bound"], "O")
@@ -353,9 +354,33 @@ def test_decode(B, H, Hkv, Lmax, d, lens, window, sinks, q4):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("q4", [False, True])
-@pytest.mark.parametrize("splits", [1, 2, 7, 64, 256])
-def test_split_counts(splits, q4):
-    _run_decode(q4, _case(2, 6, 2, 2100, 128, [2100, 930], seed=11), 2000, 6, splits)
+def test_ragged_batch_with_empty_sequences(q4):
+    """Sequences of one chunk, several, and none."""
+    lens = [700, 0, 0, 65, 64, 1, 1300, 0, 129, 5] * 5 + [0]
+    _run_decode(q4, _case(len(lens), 16, 16, 1300, 64, lens, seed=11), 1200, 6)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q4", [False, True])
+def test_many_sequences(q4):
+    """Short ragged sequences."""
+    lens = [(37 * i) % 150 for i in range(101)]
+    _run_decode(q4, _case(101, 2, 1, 150, 64, lens, seed=17), 100, 3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q4", [False, True])
+def test_one_long_sequence(q4):
+    """One unit in many chunks."""
+    _run_decode(q4, _case(1, 3, 1, 20000, 128, [19999], seed=18), 1 << 20, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q4", [False, True])
+def test_same_bits_every_time(q4):
+    case = _case(7, 8, 2, 900, 128, [900, 3, 450, 899, 0, 77, 64], seed=19)
+    a, b = _run_decode(q4, case, 800, 4), _run_decode(q4, case, 800, 4)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 @pytest.mark.gpu

@@ -965,7 +965,7 @@ static fa_status make_kv4(fa::Kv4RowsParams* p, const void* a, const void* b, co
   if (!aligned16(a) || !aligned16(b) || !aligned16(k_codes) || !aligned16(k_steps) || !aligned16(v_codes) ||
       !aligned16(v_steps) || (reinterpret_cast<uintptr_t>(starts) & 3u) || (reinterpret_cast<uintptr_t>(lens) & 3u))
     return FA_ERR_MISALIGNED;
-  if ((rows * (d / 8) + 255) / 256 > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  if (rows > 0x7fffffffLL - 256) return FA_ERR_UNSUPPORTED;  // 256 GB of rows
   p->codes[0] = static_cast<uint8_t*>(const_cast<void*>(k_codes));
   p->codes[1] = static_cast<uint8_t*>(const_cast<void*>(v_codes));
   p->steps[0] = static_cast<__nv_bfloat16*>(const_cast<void*>(k_steps));
@@ -976,7 +976,7 @@ static fa_status make_kv4(fa::Kv4RowsParams* p, const void* a, const void* b, co
   p->out[1] = static_cast<__nv_bfloat16*>(const_cast<void*>(b));
   p->starts = starts;
   p->lens = lens;
-  p->rows = rows;
+  p->rows = (unsigned)rows;
   p->Hkv = Hkv;
   p->T = T;
   p->Lmax = Lmax;
@@ -988,12 +988,14 @@ fa_status fa_kv4_write(const void* k, const void* v, void* k_codes, void* k_step
   fa::Kv4RowsParams p;
   const fa_status st = make_kv4(&p, k, v, k_codes, k_steps, v_codes, v_steps, starts, lens, B, Hkv, T, Lmax, d);
   if (st != FA_OK || p.rows == 0) return st;
-  const dim3 grid((unsigned)((p.rows * (d / 8) + 255) / 256), 2);
+  const unsigned per_block = 2048u / (unsigned)d;  // rows of a block, one a thread
+  const bool many = p.rows / (4 * per_block) >= 148u;
+  const dim3 grid((p.rows + (many ? 4 : 1) * per_block - 1) / ((many ? 4 : 1) * per_block), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
-    fa::fa_kv4_write_kernel<64><<<grid, 256, 0, s>>>(p);
+    many ? fa::fa_kv4_write_kernel<64, 4><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_write_kernel<64, 1><<<grid, 256, 0, s>>>(p);
   else
-    fa::fa_kv4_write_kernel<128><<<grid, 256, 0, s>>>(p);
+    many ? fa::fa_kv4_write_kernel<128, 4><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_write_kernel<128, 1><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -1003,12 +1005,14 @@ fa_status fa_kv4_read(const void* k_codes, const void* k_steps, const void* v_co
   fa::Kv4RowsParams p;
   const fa_status st = make_kv4(&p, k, v, k_codes, k_steps, v_codes, v_steps, starts, lens, B, Hkv, T, Lmax, d);
   if (st != FA_OK || p.rows == 0) return st;
-  const dim3 grid((unsigned)((p.rows * (d / 8) + 255) / 256), 2);
+  const unsigned per_block = 2048u / (unsigned)d;  // rows of a block, one a thread
+  const bool many = p.rows / (4 * per_block) >= 148u;
+  const dim3 grid((p.rows + (many ? 4 : 1) * per_block - 1) / ((many ? 4 : 1) * per_block), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
-    fa::fa_kv4_read_kernel<64><<<grid, 256, 0, s>>>(p);
+    many ? fa::fa_kv4_read_kernel<64, 4><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_read_kernel<64, 1><<<grid, 256, 0, s>>>(p);
   else
-    fa::fa_kv4_read_kernel<128><<<grid, 256, 0, s>>>(p);
+    many ? fa::fa_kv4_read_kernel<128, 4><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_read_kernel<128, 1><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -27,19 +27,49 @@ struct Kv4RowsParams {
   __nv_bfloat16* steps[2];    // [B, Hkv, Lmax, d / 32]
   const int* starts;          // [B] position of each sequence's first row, or null (0)
   const int* lens;            // [B] rows of each sequence, or null (T)
-  long long rows;             // B * Hkv * T
+  unsigned rows;              // B * Hkv * T
   int Hkv, T, Lmax;
 };
 
-// Cache row of row `r` of the [B, Hkv, T] rows, or -1 where it lies past the sequence's rows or outside the
-// cache.
-__device__ __forceinline__ long long kv4_cache_row(const Kv4RowsParams& p, long long r) {
-  const long long bh = r / p.T;
-  const int t = (int)(r - bh * p.T);
-  const int b = (int)(bh / p.Hkv);
-  const long long pos = (p.starts ? (long long)__ldg(p.starts + b) : 0ll) + t;
-  if (t >= (p.lens ? __ldg(p.lens + b) : p.T) || pos < 0 || pos >= p.Lmax) return -1;
-  return bh * p.Lmax + pos;
+// Walks a thread's rows of [B, Hkv, T]: row(): the cache row of the current one, or -1 where it lies past the
+// sequence's rows or outside the cache (or past all rows).
+struct Kv4Walk {
+  const Kv4RowsParams& p;
+  unsigned r, bh;
+  int t, start, len;
+
+  __device__ __forceinline__ Kv4Walk(const Kv4RowsParams& params, unsigned row0) : p(params), r(row0) {
+    bh = r / (unsigned)p.T;
+    t = (int)(r - bh * p.T);
+    sequence();
+  }
+  __device__ __forceinline__ void sequence() {
+    if (r >= p.rows) return;
+    const int b = (int)(bh / (unsigned)p.Hkv);
+    start = p.starts ? __ldg(p.starts + b) : 0;
+    len = p.lens ? min(__ldg(p.lens + b), p.T) : p.T;
+  }
+  __device__ __forceinline__ long long row() const {
+    if (r >= p.rows || t >= len) return -1;
+    const long long pos = (long long)start + t;
+    return pos < 0 || pos >= p.Lmax ? -1 : (long long)bh * p.Lmax + pos;
+  }
+  __device__ __forceinline__ void advance(int by) {
+    r += by;
+    t += by;
+    if (t >= p.T) {
+      const unsigned over = (unsigned)t / (unsigned)p.T;
+      bh += over;
+      t -= (int)over * p.T;
+      sequence();
+    }
+  }
+};
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // The largest magnitude of a group, from its bf16 words' sign-free bits (which order like the magnitudes, with
@@ -51,88 +81,140 @@ __device__ __forceinline__ uint32_t kv4_group_max(const uint4& v) {
   return max(m & 0xffffu, m >> 16);
 }
 
-// Code of x in a group of the given step (inv = 1 / step).  x and step have 8 significant bits each, so
-// x / step is a tie (n + 1/2) exactly or at least 2^-10 away from one: rounding the product x * inv to a
-// multiple of 2^-11 first (adding and taking away 1.5 * 2^12) restores the ties that the rounding of inv lost,
-// and round_half_even then agrees with the exact quotient.
-__device__ __forceinline__ uint32_t kv4_code(float x, float inv) {
-  const float q = __fadd_rn(__fadd_rn(x * inv, 6144.f), -6144.f);
-  const float n = fminf(fmaxf(rintf(q), -7.f), 7.f);
-  return __float_as_uint(n + 12582920.f) & 0xfu;  // 1.5 * 2^23 + 8: the sum's low bits are n + 8
+// Bits of 1.5 * 2^23 + (code of x in a group of the given step), for pairs of quotients q = x / step that are good to
+// 2^-20.  x and step have 8 significant bits each, so x / step is a tie (n + 1/2) exactly or at least 2^-10 away from
+// one: rounding q to a multiple of 2^-11 first (adding and taking away 1.5 * 2^12) restores the ties, and adding
+// 1.5 * 2^23 + 8 then rounds half to even.
+__device__ __forceinline__ uint2 kv4_code_bits(float2 q) {
+  const float2 a = fadd2(fadd2(q, make_float2(6144.f, 6144.f)), make_float2(-6144.f, -6144.f));
+  const float2 c = fadd2(a, make_float2(12582920.f, 12582920.f));
+  return make_uint2(__float_as_uint(c.x), __float_as_uint(c.y));
+}
+// Eight codes, the first in the lowest nibble, from their kv4_code_bits: the constant part of the bits comes off at
+// the end (mod 2^32).
+__device__ __forceinline__ uint32_t kv4_pack(const uint2 (&c)[4]) {
+  uint32_t acc = c[3].y;
+  acc = acc * 16u + c[3].x;
+#pragma unroll
+  for (int k = 2; k >= 0; --k) {
+    acc = acc * 16u + c[k].y;
+    acc = acc * 16u + c[k].x;
+  }
+  return acc - 0x4b400000u * 0x11111111u;
 }
 
-template <int D>
+// R rows per thread, whose loads are in flight together: 4 where that still leaves every SM two blocks, else 1.
+template <int D, int R>
 __global__ void __launch_bounds__(256) fa_kv4_write_kernel(const Kv4RowsParams p) {
   constexpr int TPR = D / 8;  // threads per row
   constexpr int NG = D / kKv4Group;
   const int which = blockIdx.y;  // 0: K, 1: V
-  const long long r = (blockIdx.x * 256ll + threadIdx.x) / TPR;
+  const __nv_bfloat16* x = which ? p.x[1] : p.x[0];
+  uint8_t* out = which ? p.codes[1] : p.codes[0];
+  __nv_bfloat16* steps = which ? p.steps[1] : p.steps[0];
+  const unsigned r0 = blockIdx.x * (256u / TPR * R) + threadIdx.x / TPR;
   const int i = threadIdx.x % TPR;
   const int w = i / 4, u = i % 4;  // group, and the thread's place in it
-  const long long dst = r < p.rows ? kv4_cache_row(p, r) : -1;
-  uint4 v = make_uint4(0u, 0u, 0u, 0u);
-  if (dst >= 0) v = *reinterpret_cast<const uint4*>((which ? p.x[1] : p.x[0]) + r * D + 8 * i);
-  const uint32_t amax = kv4_group_max(v);
-  __nv_bfloat16 step = __float2bfloat16(__fdiv_rn(__uint_as_float(amax << 16), 7.f));
-  const float s = __bfloat162float(step);
-  const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-  uint32_t codes = 0;
-  if (amax >= 0x7f80u) {
-    step = __ushort_as_bfloat16((unsigned short)0x7fff);
-    codes = 0x88888888u;
-  } else if (s >= 0x1p-100f) {
-    const float inv = __fdiv_rn(1.f, s);
+  long long dst[R];
+  uint4 val[R];
+  Kv4Walk walk(p, r0);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      codes |= (kv4_code(bf16lo_to_f32(word[k]), inv) << (8 * k)) | (kv4_code(bf16hi_to_f32(word[k]), inv) << (8 * k + 4));
-  } else {
-    // Steps whose reciprocal is out of range, and 0: the quotients by division.
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float x = (k & 1) ? bf16hi_to_f32(word[k / 2]) : bf16lo_to_f32(word[k / 2]);
-      codes |= kv4_code(s > 0.f ? __fdiv_rn(x, s) : 0.f, 1.f) << (4 * k);
-    }
+  for (int n = 0; n < R; ++n) {
+    if (n > 0) walk.advance(256 / TPR);
+    dst[n] = walk.row();
+    val[n] = make_uint4(0u, 0u, 0u, 0u);
+    if (dst[n] >= 0) val[n] = __ldcs(reinterpret_cast<const uint4*>(x + (size_t)(r0 + n * (256u / TPR)) * D + 8 * i));
   }
-  // V: the thread's two units (4 codes each) lie d / 32 half-words apart; lanes of neighbouring groups trade
-  // halves so that each stores one word.
-  const uint32_t give = (w & 1) ? codes & 0xffffu : codes >> 16;
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 4);
-  if (dst < 0) return;
-  uint32_t* row = reinterpret_cast<uint32_t*>((which ? p.codes[1] : p.codes[0]) + dst * (D / 2));
-  if (which == 0)
-    row[u * NG + w] = codes;
-  else if (w & 1)
-    row[((2 * u + 1) * NG + w - 1) / 2] = got | (codes & 0xffff0000u);
-  else
-    row[(2 * u * NG + w) / 2] = (codes & 0xffffu) | (got << 16);
-  if (u == 0) (which ? p.steps[1] : p.steps[0])[dst * NG + w] = step;
+#pragma unroll
+  for (int n = 0; n < R; ++n) {
+    const uint4 v = val[n];
+    const uint32_t amax = kv4_group_max(v);
+    // amax / 7 is never within 2^-12 of a bf16 tie (amax has 8 bits), so the fp32 product rounds like the quotient.
+    __nv_bfloat16 step = __float2bfloat16(__uint_as_float(amax << 16) * (1.f / 7.f));
+    const float s = __bfloat162float(step);
+    const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+    uint32_t codes = 0;
+    if (amax >= 0x7f80u) {
+      step = __ushort_as_bfloat16((unsigned short)0x7fff);
+      codes = 0x88888888u;
+    } else if (s >= 0x1p-100f) {  // |x / step| < 7.03: no clamp
+      const float inv = rcp_approx(s);
+      uint2 c[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        c[k] = kv4_code_bits(fmul2(make_float2(bf16lo_to_f32(word[k]), bf16hi_to_f32(word[k])), make_float2(inv, inv)));
+      codes = kv4_pack(c);
+    } else {
+      // Steps down to 0, rounded to few bits or to none: quotients by division, clamped.
+      auto q = [&](float y) { return s > 0.f ? fminf(fmaxf(__fdiv_rn(y, s), -7.f), 7.f) : 0.f; };
+      uint2 c[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        c[k] = kv4_code_bits(make_float2(q(bf16lo_to_f32(word[k])), q(bf16hi_to_f32(word[k]))));
+      codes = kv4_pack(c);
+    }
+    // V: the thread's two units (4 codes each) lie d / 32 half-words apart; lanes of neighbouring groups trade
+    // halves so that each stores one word.
+    const uint32_t give = (w & 1) ? codes & 0xffffu : codes >> 16;
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 4);
+    if (dst[n] < 0) continue;
+    uint32_t* row = reinterpret_cast<uint32_t*>(out + dst[n] * (D / 2));
+    if (which == 0)
+      row[u * NG + w] = codes;
+    else if (w & 1)
+      row[((2 * u + 1) * NG + w - 1) / 2] = got | (codes & 0xffff0000u);
+    else
+      row[(2 * u * NG + w) / 2] = (codes & 0xffffu) | (got << 16);
+    if (u == 0) steps[dst[n] * NG + w] = step;
+  }
 }
 
-template <int D>
+template <int D, int R>
 __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const Kv4RowsParams p) {
   constexpr int TPR = D / 8;
   constexpr int NG = D / kKv4Group;
   const int which = blockIdx.y;
-  const long long r = (blockIdx.x * 256ll + threadIdx.x) / TPR;
+  const uint8_t* in = which ? p.codes[1] : p.codes[0];
+  const __nv_bfloat16* steps = which ? p.steps[1] : p.steps[0];
+  __nv_bfloat16* out = which ? p.out[1] : p.out[0];
+  const unsigned r0 = blockIdx.x * (256u / TPR * R) + threadIdx.x / TPR;
   const int i = threadIdx.x % TPR;
   const int w = i / 4, u = i % 4;
-  const long long src = r < p.rows ? kv4_cache_row(p, r) : -1;
-  uint32_t codes = 0;
-  float s = 0.f;
-  if (src >= 0) {
-    const uint32_t* row = reinterpret_cast<const uint32_t*>((which ? p.codes[1] : p.codes[0]) + src * (D / 2));
-    codes = which == 0 ? row[u * NG + w] : row[(w & 1) ? ((2 * u + 1) * NG + w - 1) / 2 : (2 * u * NG + w) / 2];
-    s = __bfloat162float((which ? p.steps[1] : p.steps[0])[src * NG + w]);
-  }
-  const uint32_t give = (w & 1) ? codes & 0xffffu : codes >> 16;
-  const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 4);
-  if (src < 0) return;
-  if (which == 1) codes = (w & 1) ? got | (codes & 0xffff0000u) : (codes & 0xffffu) | (got << 16);
-  uint32_t o[4];
+  const int at = which == 0 ? u * NG + w : ((w & 1) ? ((2 * u + 1) * NG + w - 1) / 2 : (2 * u * NG + w) / 2);
+  bool live[R];
+  uint32_t word[R];
+  float st[R];
+  Kv4Walk walk(p, r0);
 #pragma unroll
-  for (int k = 0; k < 4; ++k)  // step * (code - 8) is exact in fp32; one rounding to bf16
-    o[k] = pack_bf16x2(s * (float)((int)((codes >> (8 * k)) & 0xfu) - 8), s * (float)((int)((codes >> (8 * k + 4)) & 0xfu) - 8));
-  *reinterpret_cast<uint4*>((which ? p.out[1] : p.out[0]) + r * D + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+  for (int n = 0; n < R; ++n) {
+    if (n > 0) walk.advance(256 / TPR);
+    const long long src = walk.row();
+    live[n] = src >= 0;
+    word[n] = 0;
+    st[n] = 0.f;
+    if (live[n]) {
+      word[n] = reinterpret_cast<const uint32_t*>(in + src * (D / 2))[at];
+      st[n] = __bfloat162float(steps[src * NG + w]);
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < R; ++n) {
+    uint32_t codes = word[n];
+    const uint32_t give = (w & 1) ? codes & 0xffffu : codes >> 16;
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 4);
+    if (!live[n]) continue;
+    if (which == 1) codes = (w & 1) ? got | (codes & 0xffff0000u) : (codes & 0xffffu) | (got << 16);
+    // code - 8 from the low bits of 2^23 + code; step * (code - 8) is exact in fp32; one rounding to bf16.
+    auto with = [&](int k) { return __uint_as_float(0x4b000000u | ((codes >> (4 * k)) & 0xfu)); };
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 c = fadd2(make_float2(with(2 * k), with(2 * k + 1)), make_float2(-8388616.f, -8388616.f));
+      const float2 y = fmul2(c, make_float2(st[n], st[n]));
+      o[k] = pack_bf16x2(y.x, y.y);
+    }
+    __stcs(reinterpret_cast<uint4*>(out + (size_t)(r0 + n * (256u / TPR)) * D + 8 * i), make_uint4(o[0], o[1], o[2], o[3]));
+  }
 }
 
 }  // namespace fa

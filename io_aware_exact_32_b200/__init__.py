@@ -168,12 +168,15 @@ def _check(code: int, where: str):
 
 
 def _need(t, name, dtype, device, shape=None):
+    try:  # the good case first, by the cheapest questions (get_device: -1 on the host, where index is None)
+        if t.dtype is dtype and t.get_device() == device.index and t.is_contiguous() and \
+                (shape is None or t.shape == shape):
+            return
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype is dtype and device.type == "cuda" and t.device == device and t.is_contiguous() and \
-            (shape is None or t.shape == shape):
-        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device.type != "cuda":
@@ -686,8 +689,8 @@ def attention_forward_fp8(q, k, v, causal: bool = False, scale=None, signs=None,
 def attention_forward_window(q, k, v, window: int, sinks: int = 0, scale=None, stream=None):
     """Allocate O and LSE and run fa_fwd_window; returns (o, lse)."""
     import torch
-    B, H, Nq, d = q.shape
-    o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=q.device)
+    B, H, Nq, _ = q.shape
+    o = torch.empty_like(q)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     fa_fwd_window(q, k, v, o, lse, window, sinks, scale, stream)
     return o, lse

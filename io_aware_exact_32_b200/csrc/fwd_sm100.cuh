@@ -85,6 +85,9 @@ struct FwdTraits {
   static constexpr int WARP_BIAS = 10;
   static constexpr int THREADS = EXT ? 352 : 320;
   static constexpr uint32_t IDESC_QK = F8 ? make_idesc_e4m3(128, 128, false, false) : make_idesc_bf16(128, 128, false, false);
+  // Sink tiles of at most 32 visible keys (window instantiation).
+  static constexpr int SHORT = 32;
+  static constexpr uint32_t IDESC_QK_SHORT = make_idesc_bf16(128, SHORT, false, false);
   static constexpr uint32_t IDESC_PV = F8 ? make_idesc_e4m3(128, D, false, true) : make_idesc_bf16(128, D, false, true);
 };
 
@@ -144,7 +147,8 @@ __device__ __forceinline__ int fwd_num_kv_tiles(int q0, int span, int Nq, int Nk
 }
 
 template <int D, bool F8>
-__device__ __forceinline__ void fwd_issue_qk(uint32_t tmem_d, uint32_t q_smem, uint32_t k_smem) {
+__device__ __forceinline__ void fwd_issue_qk(uint32_t tmem_d, uint32_t q_smem, uint32_t k_smem,
+                                             uint32_t idesc = FwdTraits<D, F8>::IDESC_QK) {
   using T = FwdTraits<D, F8>;
   const uint64_t qd = make_sdesc_sw128(q_smem, 16, 1024), kd = make_sdesc_sw128(k_smem, 16, 1024);
 #pragma unroll
@@ -152,9 +156,9 @@ __device__ __forceinline__ void fwd_issue_qk(uint32_t tmem_d, uint32_t q_smem, u
     // K advances 32 bytes inside a 128-byte swizzle row; every 4 steps, the next box.
     const uint64_t off = (uint64_t)(((kk / 4) * T::BOX_BYTES + (kk % 4) * 32) >> 4);
     if constexpr (F8)
-      mma_ss_w_f8(tmem_d, qd + off, kd + off, T::IDESC_QK, kk > 0 ? 1u : 0u);
+      mma_ss_w_f8(tmem_d, qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
     else
-      mma_ss_w(tmem_d, qd + off, kd + off, T::IDESC_QK, kk > 0 ? 1u : 0u);
+      mma_ss_w(tmem_d, qd + off, kd + off, idesc, kk > 0 ? 1u : 0u);
   }
 }
 
@@ -177,6 +181,17 @@ __device__ __forceinline__ void fwd_issue_pv(uint32_t tmem_d, uint32_t tmem_p, u
     else
       mma_ts_w(tmem_d, tmem_p + kk * 8, vd + voff, T::IDESC_PV, (accumulate || kk > 0) ? 1u : 0u);
   }
+}
+
+// O += P V over the first SHORT keys of the tile.
+template <int D>
+__device__ __forceinline__ void fwd_issue_pv_short(uint32_t tmem_d, uint32_t tmem_p, uint32_t v_smem, bool accumulate) {
+  using T = FwdTraits<D>;
+  const uint64_t vd = make_sdesc_sw128(v_smem, T::BOX_BYTES, 1024);
+#pragma unroll
+  for (int kk = 0; kk < T::SHORT / T::KSTEP; ++kk)
+    mma_ts_w(tmem_d, tmem_p + kk * 8, vd + (uint64_t)((kk * T::KSTEP * 128) >> 4), T::IDESC_PV,
+             (accumulate || kk > 0) ? 1u : 0u);
 }
 
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
@@ -253,6 +268,9 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
   const int G = gridDim.x;
   // Key tile of entry j of an item's list.
   auto key_tile = [](const FwdItem& w, int j) -> int { return WIN ? (j < w.s ? j : j - w.s + w.lo) : j; };
+  // Whether entry j is a sink tile of at most SHORT visible keys: those are then all its rows see of it, and only
+  // they are computed (a tile of a few sinks costs a fifth of a full one).
+  auto is_short = [&](const FwdItem& w, int j) -> bool { return WIN && j < w.s && p.sinks - 128 * j <= T::SHORT; };
   auto item_at = [&](int r) -> int { return r * G + ((r & 1) ? (G - 1 - (int)blockIdx.x) : (int)blockIdx.x); };
   auto decode = [&](int i) -> FwdItem {
     FwdItem w;
@@ -368,6 +386,64 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         int j = two ? step : 2 * step + t;  // entry of the item's list, then its key tile
         if constexpr (WIN) {
           if (two && t == 1 && step >= w.x0) j += w.x1 - w.x0;
+          if (is_short(w, j)) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_S_FULL + t), (cnt + step) & 1, abort_flag)))) break;
+            tc_fence_after();
+            uint32_t sw[T::SHORT];
+            tmem_ld32x32b_x32_wait(lane_addr + colS, sw);
+            float* s = reinterpret_cast<float*>(sw);
+            const int n_vis = p.sinks - 128 * j;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < T::SHORT; ++c) {
+              s[c] = c < n_vis ? s[c] : -INFINITY;
+              mx = fmaxf(mx, s[c]);
+            }
+            // The sink tiles come first: the maximum moves as in a full tile, and whatever O holds is rescaled.
+            const float m_tile = mx * scale_log2;
+            float alpha = 1.f;
+            bool resc = false;
+            if (m_tile > m_run + kRescaleThreshold) {
+              alpha = ex2_approx(m_run - m_tile);
+              resc = (step > 0) && (m_run != -INFINITY);
+              m_run = m_tile;
+            }
+            const float base = (m_run == -INFINITY) ? 0.f : m_run;
+            uint32_t pk[T::SHORT / 2];
+            float sum_e = 0.f, sum_r = 0.f;
+#pragma unroll
+            for (int c = 0; c < T::SHORT / 2; ++c) {
+              const float e0 = ex2_approx(fmaf(s[2 * c], scale_log2, -base));
+              const float e1 = ex2_approx(fmaf(s[2 * c + 1], scale_log2, -base));
+              pk[c] = pack_bf16x2(e0, e1);
+              sum_e += e0 + e1;
+              sum_r += bf16lo_to_f32(pk[c]) + bf16hi_to_f32(pk[c]);
+            }
+            tmem_st32x32b_x16(lane_addr + colS, pk);
+            if (__any_sync(0xffffffffu, resc)) {
+              ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_O_DONE + t), (cnt + step - 1) & 1, abort_flag));
+              if (ok) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                  uint32_t o[16];
+                  tmem_ld32x32b_x16_wait(lane_addr + colO + 16 * c, o);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                  tmem_st32x32b_x16(lane_addr + colO + 16 * c, o);
+                }
+              }
+            }
+            tmem_st_wait();
+            if (!ok) break;
+            tc_fence_before();
+            // Both halves' barriers, so that their phases go on counting tiles (the issuer waits for the first).
+            mbar_arrive(bar(T::BAR_P_READY + 2 * t));
+            mbar_arrive(bar(T::BAR_P_READY + 2 * t + 1));
+            l_run = l_run * alpha + sum_e;
+            lr_run = lr_run * alpha + sum_r;
+            continue;
+          }
           j = key_tile(w, j);
         }
         ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_S_FULL + t), (cnt + step) & 1, abort_flag));
@@ -628,7 +704,14 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
       const uint32_t tO[2] = {tmem_base + T::col_o(0), tmem_base + T::col_o(1)};
       // O_t += P_t V (V of load v_load): the first key half as soon as group t has published it, then
       // the second; c counts group t's tiles (barrier phase), acc: whether O_t already holds a sum.
-      auto pv = [&](int t, int c, int v_load, bool acc) -> bool {
+      auto pv = [&](int t, int c, int v_load, bool acc, bool shrt) -> bool {
+        if (WIN && shrt) {
+          if (!warp_wait(bar(T::BAR_P_READY + 2 * t), c & 1, abort_flag)) return false;
+          tc_fence_after();
+          fwd_issue_pv_short<D>(tO[t], tS[t], kv_smem(v_load), acc);
+          mma_commit_w(bar(T::BAR_O_DONE + t));
+          return true;
+        }
         for (int half = 0; half < 2; ++half) {
           if (!warp_wait(bar(T::BAR_P_READY + 2 * t + half), c & 1, abort_flag)) return false;
           tc_fence_after();
@@ -636,6 +719,10 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         }
         mma_commit_w(bar(T::BAR_O_DONE + t));
         return true;
+      };
+      auto qk = [&](int t, uint32_t q, int k_load, bool shrt) {
+        fwd_issue_qk<D, F8>(tS[t], q, kv_smem(k_load), WIN && shrt ? T::IDESC_QK_SHORT : T::IDESC_QK);
+        mma_commit_w(bar(T::BAR_S_FULL + t));
       };
       bool ok = true;
       int L = 0;                // global index of the item's first K/V load
@@ -663,30 +750,28 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
             const bool has1 = 2 * i + 1 < n_kv;
             if (!(ok = kv_wait(ik0))) break;
             tc_fence_after();
-            fwd_issue_qk<D, F8>(tS[0], q_smem[0], kv_smem(ik0));
-            mma_commit_w(bar(T::BAR_S_FULL + 0));
+            qk(0, q_smem[0], ik0, is_short(w, 2 * i));
             release(ik0);
             if (v1_prev >= 0) {
               if (!(ok = kv_wait(v1_prev))) break;
-              if (!(ok = pv(1, cnt1 + i - 1, v1_prev, i - 1 > 0))) break;
+              if (!(ok = pv(1, cnt1 + i - 1, v1_prev, i - 1 > 0, is_short(w, 2 * i - 1)))) break;
               release(v1_prev);
               v1_prev = -1;
             }
             if (has1) {
               if (!(ok = kv_wait(ik1))) break;
               tc_fence_after();
-              fwd_issue_qk<D, F8>(tS[1], q_smem[0], kv_smem(ik1));
-              mma_commit_w(bar(T::BAR_S_FULL + 1));
+              qk(1, q_smem[0], ik1, is_short(w, 2 * i + 1));
               release(ik1);
               v1_prev = iv1;
             }
             if (!(ok = kv_wait(iv0))) break;
-            if (!(ok = pv(0, cnt0 + i, iv0, i > 0))) break;
+            if (!(ok = pv(0, cnt0 + i, iv0, i > 0, is_short(w, 2 * i)))) break;
             release(iv0);
           }
           if (ok && v1_prev >= 0) {
             const int i = nsteps - 1;
-            if ((ok = kv_wait(v1_prev)) && (ok = pv(1, cnt1 + i, v1_prev, i > 0))) release(v1_prev);
+            if ((ok = kv_wait(v1_prev)) && (ok = pv(1, cnt1 + i, v1_prev, i > 0, is_short(w, 2 * i + 1)))) release(v1_prev);
           }
           cnt0 += (n_kv + 1) / 2;
           cnt1 += n_kv / 2;
@@ -695,9 +780,10 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
           // cannot see (j >= n0), tile 1 visits all n_kv (WIN: all but [x0, x1)).
           int v_prev = -1;  // load index of the V tile of tile 1's pending P V
           int d1 = 0;       // P V products of tile 1 issued
+          bool short1 = false;  // the pending one's tile is short
           auto flush1 = [&]() -> bool {
             if (d1 == 0 && !o_free(1)) return false;
-            if (!pv(1, cnt1 + d1, v_prev, d1 > 0)) return false;
+            if (!pv(1, cnt1 + d1, v_prev, d1 > 0, short1)) return false;
             release(v_prev);
             ++d1;
             v_prev = -1;
@@ -708,21 +794,17 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
             const bool has1 = !WIN || j < w.x0 || j >= w.x1;
             if (!(ok = kv_wait(ik))) break;
             tc_fence_after();
-            if (j < w.n0) {
-              fwd_issue_qk<D, F8>(tS[0], q_smem[0], kv_smem(ik));
-              mma_commit_w(bar(T::BAR_S_FULL + 0));
-            }
+            const bool shrt = is_short(w, j);
+            if (j < w.n0) qk(0, q_smem[0], ik, shrt);
             if (v_prev >= 0 && !(ok = flush1())) break;
-            if (has1) {
-              fwd_issue_qk<D, F8>(tS[1], q_smem[1], kv_smem(ik));
-              mma_commit_w(bar(T::BAR_S_FULL + 1));
-            }
+            if (has1) qk(1, q_smem[1], ik, shrt);
             release(ik);
             if (!(ok = kv_wait(iv))) break;
             if (j < w.n0) {
               if (j == 0 && !(ok = o_free(0))) break;
-              if (!(ok = pv(0, cnt0 + j, iv, j > 0))) break;
+              if (!(ok = pv(0, cnt0 + j, iv, j > 0, shrt))) break;
             }
+            short1 = shrt;
             if (has1)
               v_prev = iv;
             else

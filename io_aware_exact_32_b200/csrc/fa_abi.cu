@@ -234,9 +234,20 @@ fa_status launch_fwd(const void* q, const void* k, const void* v, void* o, float
   const int sms = num_sms();
   p.tiles = ((long long)((Nq + 255) / 256) * BH < sms) ? 1 : 2;
   p.nunits = (Nq + 128 * p.tiles - 1) / (128 * p.tiles);
+  p.pair = 0;
+  if constexpr (WIN) {
+    // An even number of heads to a key/value head: the two tiles are the same rows of two of them.  They then see the
+    // same key tiles, one fewer than two neighbouring row tiles do together.
+    const long long paired = (long long)((Nq + 127) / 128) * (BH / 2);
+    if (win->group % 2 == 0 && paired >= sms) {
+      p.tiles = 2;
+      p.pair = 1;
+      p.nunits = (Nq + 127) / 128;
+    }
+  }
   p.scale_log2 = scale * 1.4426950408889634f;
   p.causal = causal ? 1 : 0;
-  const long long items = (long long)p.nunits * BH;
+  const long long items = (long long)p.nunits * (p.pair ? BH / 2 : BH);
   if (items > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const long long blocks = p.tiles == 2 ? (items < sms ? items : sms) : items;
   // The kernel counts K/V loads per CTA in 32-bit integers.

@@ -116,6 +116,7 @@ struct FwdParams {
   // Sliding-window instantiation only: key j is visible to a query at position p iff j <= p and
   // (j > p - window or j < sinks); query head bh reads key/value head bh / group.
   int window, sinks, group;
+  int pair;  // the two tiles of an item: 0 neighbouring row tiles of a head, 1 the same rows of two heads of a group
 };
 
 // One work item: the query unit of rows [q0, q0 + 128 tiles) of (batch, head) bh.  n0 / n1: key tiles
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
   // even rounds, backward in odd ones), which evens out the causal work per CTA; with fewer items
   // than CTAs (the split mode) every CTA has exactly one.  Every role walks the same list, and the
   // K/V ring, the Q slots and all barrier phases run on across items.
-  const int n_items = p.nunits * p.BH;
+  const int n_items = p.nunits * (WIN && p.pair ? p.BH / 2 : p.BH);
   const int G = gridDim.x;
   // Key tile of entry j of an item's list.
   auto key_tile = [](const FwdItem& w, int j) -> int { return WIN ? (j < w.s ? j : j - w.s + w.lo) : j; };
@@ -274,10 +275,11 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
   auto item_at = [&](int r) -> int { return r * G + ((r & 1) ? (G - 1 - (int)blockIdx.x) : (int)blockIdx.x); };
   auto decode = [&](int i) -> FwdItem {
     FwdItem w;
-    w.bh = i % p.BH;
-    const int rank = i / p.BH;
+    const int heads = WIN && p.pair ? p.BH / 2 : p.BH;
+    w.bh = WIN && p.pair ? i % heads * 2 : i % heads;
+    const int rank = i / heads;
     const int unit = p.causal ? (p.nunits - 1 - rank) : rank;
-    w.q0 = unit * 128 * p.tiles;
+    w.q0 = unit * (WIN && p.pair ? 128 : 128 * p.tiles);
     w.s = w.lo = w.x0 = w.x1 = 0;
     if constexpr (WIN) {
       const int off = p.Nk - p.Nq, last = p.Nq - 1;
@@ -285,7 +287,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
       fwd_window_tiles(w.q0, min(w.q0 + 127, last), off, p.window, w.lo, hi0);
       lo1 = w.lo;
       hi1 = hi0;
-      if (two) fwd_window_tiles(min(w.q0 + 128, last), min(w.q0 + 255, last), off, p.window, lo1, hi1);
+      if (two && !p.pair) fwd_window_tiles(min(w.q0 + 128, last), min(w.q0 + 255, last), off, p.window, lo1, hi1);
       const int ns = (p.sinks + 127) / 128;
       w.s = min(ns, w.lo);
       w.n_kv = w.s + hi1 - w.lo + 1;
@@ -367,8 +369,8 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
     int bcnt = 0;  // staged bias tiles this group has consumed
     for (int it = 0; ok && item_at(it) < n_items; ++it) {
       const FwdItem w = decode(item_at(it));
-      const int bh = w.bh;
-      const int row = w.q0 + (two ? 128 * t : 0) + r;  // query index within the head
+      const int bh = WIN && p.pair ? w.bh + t : w.bh;
+      const int row = w.q0 + (two && !(WIN && p.pair) ? 128 * t : 0) + r;  // query index within the head
       const int n_own = two ? (t ? w.n1 : w.n0) : (w.n_kv + 1 - t) / 2;  // key tiles this group visits
       int kmax = p.Nk - 1;  // last visible key of this row (inclusive)
       if (p.causal) kmax = min(kmax, row + p.Nk - p.Nq);
@@ -838,7 +840,8 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         for (int t = 0; t < p.tiles; ++t)
           for (int b = 0; b < T::NBOX; ++b)
             tma_load_3d(sbase + T::OFF_Q + (2 * slot + t) * T::TILE_BYTES + b * T::BOX_BYTES, &tmQ,
-                        bar(T::BAR_Q_FULL + slot), T::BOX_COLS * b, w.q0 + 128 * t, w.bh);
+                        bar(T::BAR_Q_FULL + slot), T::BOX_COLS * b, WIN && p.pair ? w.q0 : w.q0 + 128 * t,
+                        WIN && p.pair ? w.bh + t : w.bh);
         ++q_fills[slot];
         for (int idx = 0; idx < 2 * w.n_kv; ++idx) {
           const int g = L + idx;

@@ -21,7 +21,7 @@
 //   SMEM: K_j, V_j (resident), a ring of (Q_i, dO_i) stages, dS^T (bf16, 128-byte swizzle),
 //         and at d = 64 an fp32 staging tile for the dQ block
 //   P/dS warpgroups: one thread per key row, two groups of 64 query columns each: P, dS (the
-//              critical path); at the end group 0 writes dV out and group 1 dK
+//              critical path); group 0 also runs the dK/dV epilogue
 //   dQ warpgroup: one thread per query row of the dQ block: read it out of TMEM, release the
 //              columns, then add it into the fp32 accumulator with TMA bulk reduce-adds of a staged
 //              tile (d = 64: its own staging buffer; d = 128: the block's dO tile once dV has read it)
@@ -507,15 +507,15 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       tc_fence_before();
       mbar_arrive(bar(T::BAR_DS_READY));
     }
-    // dK, dV epilogue: group 0 writes dV, group 1 dK (both groups hold the same key rows).
-    if (ok && n_q > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_ACC_DONE), 0, abort_flag));
+    // dK, dV epilogue (group 0 owns it; both groups hold the same key rows).
+    if (ok && wg == 0 && n_q > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_ACC_DONE), 0, abort_flag));
     if (!ok) {
       *abort_flag = 1;
-    } else {
+    } else if (wg == 0) {
       tc_fence_after();
       const size_t off = ((size_t)bh * p.Nk + (key_ok ? key : 0)) * D;
-      {
-        const int which = wg;
+#pragma unroll 1
+      for (int which = 0; which < 2; ++which) {
         __nv_bfloat16* out = (which ? p.dk : p.dv) + off;
         const float mul = which ? p.scale : 1.f;
 #pragma unroll 1

@@ -235,6 +235,7 @@ fa_status launch_fwd(const void* q, const void* k, const void* v, void* o, float
   p.tiles = ((long long)((Nq + 255) / 256) * BH < sms) ? 1 : 2;
   p.nunits = (Nq + 128 * p.tiles - 1) / (128 * p.tiles);
   p.pair = 0;
+  p.wide = (reinterpret_cast<uintptr_t>(o) & 31u) == 0 ? 1 : 0;
   if constexpr (WIN) {
     // An even number of heads to a key/value head: the two tiles are the same rows of two of them.  They then see the
     // same key tiles, one fewer than two neighbouring row tiles do together.

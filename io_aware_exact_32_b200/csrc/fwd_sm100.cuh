@@ -116,6 +116,7 @@ struct FwdParams {
   // Sliding-window instantiation only: key j is visible to a query at position p iff j <= p and
   // (j > p - window or j < sinks); query head bh reads key/value head bh / group.
   int window, sinks, group;
+  int wide;  // o is 32-byte aligned
   int pair;  // the two tiles of an item: 0 neighbouring row tiles of a head, 1 the same rows of two heads of a group
 };
 
@@ -129,6 +130,13 @@ struct FwdItem {
   int bh, q0, n0, n1, n_kv;
   int s, lo, x0, x1;
 };
+
+// Bits 0 .. n - 1 (all 32 from n = 32 on, none below n = 1).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  uint32_t r;
+  asm("shl.b32 %0, 1, %1;" : "=r"(r) : "r"(max(n, 0)));  // shifts of 32 and more give 0
+  return r - 1u;
+}
 
 // Key tiles [lo, hi] inside the window of query rows [a, b] (positions a + off .. b + off); rows before
 // the first key see none and visit tile 0 fully masked.
@@ -463,10 +471,23 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         [[maybe_unused]] const int wlo = kmin - 128 * j;
         [[maybe_unused]] const int slim = p.sinks - 128 * j;
         const bool masked = __any_sync(0xffffffffu, lim < 127 || (WIN && wlo > 0 && slim < 128));
+        // WIN: the visible keys of 32-key chunk i as bits (one test and one select per score, whatever hides it).
+        auto visible = [&](int i) -> uint32_t {
+          return bits_below(lim + 1 - 32 * i) & (~bits_below(wlo - 32 * i) | bits_below(slim - 32 * i));
+        };
         if (masked) {
+          if constexpr (WIN) {
+            const uint32_t v0 = visible(0), v1 = visible(1);
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c > lim || (WIN && c < wlo && c >= slim)) s[c] = -INFINITY;
+            for (int c = 0; c < 32; ++c) {
+              if (!(v0 & (1u << c))) s[c] = -INFINITY;
+              if (!(v1 & (1u << c))) s[c + 32] = -INFINITY;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c > lim) s[c] = -INFINITY;
+          }
         }
         if constexpr (EXT) {
           if (staged_bias) {
@@ -478,9 +499,18 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         const float mx_a = max64(s);
         tmem_wait_ld_x64(sb);
         if (masked) {
+          if constexpr (WIN) {
+            const uint32_t v2 = visible(2), v3 = visible(3);
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (c + 64 > lim || (WIN && c + 64 < wlo && c + 64 >= slim)) s2[c] = -INFINITY;
+            for (int c = 0; c < 32; ++c) {
+              if (!(v2 & (1u << c))) s2[c] = -INFINITY;
+              if (!(v3 & (1u << c))) s2[c + 32] = -INFINITY;
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (c + 64 > lim) s2[c] = -INFINITY;
+          }
         }
         if constexpr (EXT) {
           if (staged_bias) {
@@ -637,7 +667,13 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             wv[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-          if (in_range) {
+          if (WIN && p.wide) {
+            // Whole 32-byte sectors: a warp's stores lie in 32 rows.
+            if (in_range) {
+              st_global_v8(orow + 32 * c, wv);
+              st_global_v8(orow + 32 * c + 16, wv + 8);
+            }
+          } else if (in_range) {
             uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[i] = make_uint4(wv[4 * i], wv[4 * i + 1], wv[4 * i + 2], wv[4 * i + 3]);
@@ -780,25 +816,24 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         } else {
           // Two tiles, in the order S0 S1 PV0 S0' PV1 S1' ...; query tile 0 skips the key tiles it
           // cannot see (j >= n0), tile 1 visits all n_kv (WIN: all but [x0, x1)).
-          int v_prev = -1;  // load index of the V tile of tile 1's pending P V
-          int d1 = 0;       // P V products of tile 1 issued
+          int v_prev = -1;      // load index of the V tile of tile 1's pending P V
+          int d1 = 0;           // P V products of tile 1 issued
           bool short1 = false;  // the pending one's tile is short
-          auto flush1 = [&]() -> bool {
-            if (d1 == 0 && !o_free(1)) return false;
-            if (!pv(1, cnt1 + d1, v_prev, d1 > 0, short1)) return false;
-            release(v_prev);
-            ++d1;
-            v_prev = -1;
-            return true;
-          };
           for (int j = 0; ok && j < w.n_kv; ++j) {
             const int ik = L + 2 * j, iv = ik + 1;
             const bool has1 = !WIN || j < w.x0 || j >= w.x1;
+            const bool shrt = is_short(w, j);
             if (!(ok = kv_wait(ik))) break;
             tc_fence_after();
-            const bool shrt = is_short(w, j);
             if (j < w.n0) qk(0, q_smem[0], ik, shrt);
-            if (v_prev >= 0 && !(ok = flush1())) break;
+            if (WIN ? v_prev >= 0 : j > 0) {
+              const int done = WIN ? d1 : j - 1;
+              if (done == 0 && !(ok = o_free(1))) break;
+              if (!(ok = pv(1, cnt1 + done, v_prev, done > 0, short1))) break;
+              release(v_prev);
+              ++d1;
+              v_prev = -1;
+            }
             if (has1) qk(1, q_smem[1], ik, shrt);
             release(ik);
             if (!(ok = kv_wait(iv))) break;
@@ -812,7 +847,11 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
             else
               release(iv);
           }
-          if (ok && v_prev >= 0) ok = flush1();
+          if (ok && (!WIN || v_prev >= 0)) {
+            const int done = WIN ? d1 : w.n_kv - 1;
+            if (done == 0) ok = o_free(1);
+            if (ok && (ok = pv(1, cnt1 + done, v_prev, done > 0, short1))) release(v_prev);
+          }
           cnt0 += w.n0;
           cnt1 += w.n1;
         }

@@ -389,6 +389,16 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       // WIN: nor beyond cmax, unless it is a sink.
       const int cmax = WIN ? (key < p.sinks ? 0x7fffffff : shift - q0 + p.window - 1) : 0x7fffffff;
       const bool masked = __any_sync(0xffffffffu, !key_ok || cmin > cb || (WIN && cmax < cb + T::CW - 1));
+      // WIN: the visible query columns of this group as bits.
+      [[maybe_unused]] uint32_t vis[2];
+      if constexpr (WIN) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int c0 = cb + 32 * i;
+          const uint32_t upto = cmax < c0 + 31 ? bits_below(cmax + 1 - c0) : 0xffffffffu;
+          vis[i] = key_ok ? upto & ~bits_below(cmin - c0) : 0u;
+        }
+      }
       const float4* st4 = reinterpret_cast<const float4*>(stat);
       const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
       [[maybe_unused]] const float2 inv2 = make_float2(kLog2e / p.scale_log2, kLog2e / p.scale_log2);  // 1 / scale
@@ -436,10 +446,18 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
           float2 p01 = make_float2(ex2_approx(x01.x), ex2_approx(x01.y));
           float2 p23 = make_float2(ex2_approx(x23.x), ex2_approx(x23.y));
           if (masked) {
-            p01.x = (key_ok && c >= cmin && (!WIN || c <= cmax)) ? p01.x : 0.f;
-            p01.y = (key_ok && c + 1 >= cmin && (!WIN || c + 1 <= cmax)) ? p01.y : 0.f;
-            p23.x = (key_ok && c + 2 >= cmin && (!WIN || c + 2 <= cmax)) ? p23.x : 0.f;
-            p23.y = (key_ok && c + 3 >= cmin && (!WIN || c + 3 <= cmax)) ? p23.y : 0.f;
+            if constexpr (WIN) {
+              const uint32_t v = vis[ch >> 1], b = 1u << ((ch & 1) * 16 + i);
+              p01.x = (v & b) ? p01.x : 0.f;
+              p01.y = (v & (b << 1)) ? p01.y : 0.f;
+              p23.x = (v & (b << 2)) ? p23.x : 0.f;
+              p23.y = (v & (b << 3)) ? p23.y : 0.f;
+            } else {
+              p01.x = (key_ok && c >= cmin) ? p01.x : 0.f;
+              p01.y = (key_ok && c + 1 >= cmin) ? p01.y : 0.f;
+              p23.x = (key_ok && c + 2 >= cmin) ? p23.x : 0.f;
+              p23.y = (key_ok && c + 3 >= cmin) ? p23.y : 0.f;
+            }
           }
           float2 t01, t23;
           [[maybe_unused]] float2 z01, z23;  // EXT: dropout factors (kept: 1 / (1 - p), dropped: 0)

@@ -131,13 +131,6 @@ struct FwdItem {
   int s, lo, x0, x1;
 };
 
-// Bits 0 .. n - 1 (all 32 from n = 32 on, none below n = 1).
-__device__ __forceinline__ uint32_t bits_below(int n) {
-  uint32_t r;
-  asm("shl.b32 %0, 1, %1;" : "=r"(r) : "r"(max(n, 0)));  // shifts of 32 and more give 0
-  return r - 1u;
-}
-
 // Key tiles [lo, hi] inside the window of query rows [a, b] (positions a + off .. b + off); rows before
 // the first key see none and visit tile 0 fully masked.
 __device__ __forceinline__ void fwd_window_tiles(int a, int b, int off, int window, int& lo, int& hi) {

@@ -391,6 +391,13 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   return d;
 }
 
+// Bits 0 .. n - 1 (all 32 from n = 32 on, none below n = 1).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  uint32_t r;
+  asm("shl.b32 %0, 1, %1;" : "=r"(r) : "r"(max(n, 0)));  // shifts of 32 and more give 0
+  return r - 1u;
+}
+
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

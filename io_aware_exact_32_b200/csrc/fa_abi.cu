@@ -1000,14 +1000,14 @@ fa_status fa_kv4_write(const void* k, const void* v, void* k_codes, void* k_step
   fa::Kv4RowsParams p;
   const fa_status st = make_kv4(&p, k, v, k_codes, k_steps, v_codes, v_steps, starts, lens, B, Hkv, T, Lmax, d);
   if (st != FA_OK || p.rows == 0) return st;
-  const unsigned per_block = 2048u / (unsigned)d;  // rows of a block, one a thread
-  const bool many = p.rows / (4 * per_block) >= 148u;
-  const dim3 grid((p.rows + (many ? 4 : 1) * per_block - 1) / ((many ? 4 : 1) * per_block), 2);
+  const unsigned per_block = 4096u / (unsigned)d;  // rows of a block, one a thread
+  const bool many = p.rows / (2 * per_block) >= 148u;
+  const dim3 grid((p.rows + (many ? 2 : 1) * per_block - 1) / ((many ? 2 : 1) * per_block), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
-    many ? fa::fa_kv4_write_kernel<64, 4><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_write_kernel<64, 1><<<grid, 256, 0, s>>>(p);
+    many ? fa::fa_kv4_write_kernel<64, 2><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_write_kernel<64, 1><<<grid, 256, 0, s>>>(p);
   else
-    many ? fa::fa_kv4_write_kernel<128, 4><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_write_kernel<128, 1><<<grid, 256, 0, s>>>(p);
+    many ? fa::fa_kv4_write_kernel<128, 2><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_write_kernel<128, 1><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -1017,14 +1017,14 @@ fa_status fa_kv4_read(const void* k_codes, const void* k_steps, const void* v_co
   fa::Kv4RowsParams p;
   const fa_status st = make_kv4(&p, k, v, k_codes, k_steps, v_codes, v_steps, starts, lens, B, Hkv, T, Lmax, d);
   if (st != FA_OK || p.rows == 0) return st;
-  const unsigned per_block = 2048u / (unsigned)d;  // rows of a block, one a thread
-  const bool many = p.rows / (4 * per_block) >= 148u;
-  const dim3 grid((p.rows + (many ? 4 : 1) * per_block - 1) / ((many ? 4 : 1) * per_block), 2);
+  const unsigned per_block = 4096u / (unsigned)d;  // rows of a block, one a thread
+  const bool many = p.rows / (2 * per_block) >= 148u;
+  const dim3 grid((p.rows + (many ? 2 : 1) * per_block - 1) / ((many ? 2 : 1) * per_block), 2);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (d == 64)
-    many ? fa::fa_kv4_read_kernel<64, 4><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_read_kernel<64, 1><<<grid, 256, 0, s>>>(p);
+    many ? fa::fa_kv4_read_kernel<64, 2><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_read_kernel<64, 1><<<grid, 256, 0, s>>>(p);
   else
-    many ? fa::fa_kv4_read_kernel<128, 4><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_read_kernel<128, 1><<<grid, 256, 0, s>>>(p);
+    many ? fa::fa_kv4_read_kernel<128, 2><<<grid, 256, 0, s>>>(p) : fa::fa_kv4_read_kernel<128, 1><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

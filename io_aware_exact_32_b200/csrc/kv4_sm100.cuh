@@ -10,8 +10,11 @@
 // 4 for V), unit u of group g sits at unit position u * (d / 32) + g, a unit's first channel in its lowest
 // nibble.
 //
-// Both kernels move bytes and nothing else (2 d bytes one way, 9 d / 16 the other): a thread holds 8 channels
-// (16 bytes of bf16), four lanes a group, and each row is read and written in full 32-byte sectors.
+// Both kernels only move bytes (2 d one way, 9 d / 16 the other), but at 6.5 TB/s an SM has 4 instructions a clock for
+// 17 channels: a thread takes 16 channels of a row (two lanes a group), so that what is done once a row, a group or a
+// thread is shared by as many channels as its registers hold, and packed fp32 pairs do the arithmetic.  With 8
+// channels a thread the prompt of the measurements took 39 us, write and read back.  Each row is read and written in
+// whole 32-byte sectors.
 #pragma once
 
 #include "sm100_ptx.cuh"
@@ -72,13 +75,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// The largest magnitude of a group, from its bf16 words' sign-free bits (which order like the magnitudes, with
-// infinities and NaN on top), over the group's four lanes.
-__device__ __forceinline__ uint32_t kv4_group_max(const uint4& v) {
-  uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
-  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
-  return max(m & 0xffffu, m >> 16);
+// The largest magnitude of 16 channels, from their bf16 words' sign-free bits (which order like the magnitudes, with
+// infinities and NaN on top), in both halves.
+__device__ __forceinline__ uint32_t kv4_max(const uint4 (&v)[2]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(v[k].x & 0x7fff7fffu, v[k].y & 0x7fff7fffu),
+                             __vmaxu2(v[k].z & 0x7fff7fffu, v[k].w & 0x7fff7fffu)));
+  return __vmaxu2(m, (m >> 16) | (m << 16));
 }
 
 // Bits of 1.5 * 2^23 + (code of x in a group of the given step), for pairs of quotients q = x / step that are good to
@@ -103,10 +108,29 @@ __device__ __forceinline__ uint32_t kv4_pack(const uint2 (&c)[4]) {
   return acc - 0x4b400000u * 0x11111111u;
 }
 
-// R rows per thread, whose loads are in flight together: 4 where that still leaves every SM two blocks, else 1.
+// Eight codes of the channels in v, for a group whose step has the reciprocal inv.
+__device__ __forceinline__ uint32_t kv4_codes8(const uint4& v, float inv) {
+  const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+  uint2 c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    c[k] = kv4_code_bits(fmul2(make_float2(bf16lo_to_f32(word[k]), bf16hi_to_f32(word[k])), make_float2(inv, inv)));
+  return kv4_pack(c);
+}
+// The same for steps down to 0, rounded to few bits or to none: quotients by division, clamped.
+__device__ __noinline__ uint32_t kv4_codes8_tiny(uint4 v, float step) {
+  const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+  auto q = [&](float y) { return step > 0.f ? fminf(fmaxf(__fdiv_rn(y, step), -7.f), 7.f) : 0.f; };
+  uint2 c[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) c[k] = kv4_code_bits(make_float2(q(bf16lo_to_f32(word[k])), q(bf16hi_to_f32(word[k]))));
+  return kv4_pack(c);
+}
+
+// R rows per thread, whose loads are in flight together: 2 where that still leaves every SM two blocks, else 1.
 template <int D, int R>
 __global__ void __launch_bounds__(256) fa_kv4_write_kernel(const Kv4RowsParams p) {
-  constexpr int TPR = D / 8;  // threads per row
+  constexpr int TPR = D / 16;  // threads per row
   constexpr int NG = D / kKv4Group;
   const int which = blockIdx.y;  // 0: K, 1: V
   const __nv_bfloat16* x = which ? p.x[1] : p.x[0];
@@ -114,64 +138,64 @@ __global__ void __launch_bounds__(256) fa_kv4_write_kernel(const Kv4RowsParams p
   __nv_bfloat16* steps = which ? p.steps[1] : p.steps[0];
   const unsigned r0 = blockIdx.x * (256u / TPR * R) + threadIdx.x / TPR;
   const int i = threadIdx.x % TPR;
-  const int w = i / 4, u = i % 4;  // group, and the thread's place in it
+  const int w = i / 2, h = i % 2;  // group, and its half that this thread has
+  // The thread's two words of a row: K, units 2 h and 2 h + 1 of its group; V (units 4 h .. 4 h + 3), those two words
+  // of its group and its neighbour's that fall to it: an even group's thread has units 4 h, 4 h + 1, an odd one's the
+  // other two.
+  const int at0 = which == 0 ? 2 * h * NG + w : ((4 * h + 2 * (w & 1)) * NG + (w & ~1)) / 2;
+  const int at1 = at0 + (which == 0 ? NG : NG / 2);
   long long dst[R];
-  uint4 val[R];
+  uint4 val[R][2];
   Kv4Walk walk(p, r0);
 #pragma unroll
   for (int n = 0; n < R; ++n) {
     if (n > 0) walk.advance(256 / TPR);
     dst[n] = walk.row();
-    val[n] = make_uint4(0u, 0u, 0u, 0u);
-    if (dst[n] >= 0) val[n] = __ldcs(reinterpret_cast<const uint4*>(x + (size_t)(r0 + n * (256u / TPR)) * D + 8 * i));
+    val[n][0] = val[n][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (dst[n] >= 0) {
+      const uint4* src = reinterpret_cast<const uint4*>(x + (size_t)(r0 + n * (256u / TPR)) * D + 16 * i);
+      val[n][0] = __ldcs(src);
+      val[n][1] = __ldcs(src + 1);
+    }
   }
 #pragma unroll
   for (int n = 0; n < R; ++n) {
-    const uint4 v = val[n];
-    const uint32_t amax = kv4_group_max(v);
+    if (__all_sync(0xffffffffu, dst[n] < 0)) continue;
+    uint32_t amax = kv4_max(val[n]);
+    amax = __vmaxu2(amax, __shfl_xor_sync(0xffffffffu, amax, 1)) & 0xffffu;
     // amax / 7 is never within 2^-12 of a bf16 tie (amax has 8 bits), so the fp32 product rounds like the quotient.
     __nv_bfloat16 step = __float2bfloat16(__uint_as_float(amax << 16) * (1.f / 7.f));
     const float s = __bfloat162float(step);
-    const uint32_t word[4] = {v.x, v.y, v.z, v.w};
-    uint32_t codes = 0;
+    uint32_t c0, c1;
     if (amax >= 0x7f80u) {
       step = __ushort_as_bfloat16((unsigned short)0x7fff);
-      codes = 0x88888888u;
+      c0 = c1 = 0x88888888u;
     } else if (s >= 0x1p-100f) {  // |x / step| < 7.03: no clamp
       const float inv = rcp_approx(s);
-      uint2 c[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        c[k] = kv4_code_bits(fmul2(make_float2(bf16lo_to_f32(word[k]), bf16hi_to_f32(word[k])), make_float2(inv, inv)));
-      codes = kv4_pack(c);
+      c0 = kv4_codes8(val[n][0], inv);
+      c1 = kv4_codes8(val[n][1], inv);
     } else {
-      // Steps down to 0, rounded to few bits or to none: quotients by division, clamped.
-      auto q = [&](float y) { return s > 0.f ? fminf(fmaxf(__fdiv_rn(y, s), -7.f), 7.f) : 0.f; };
-      uint2 c[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        c[k] = kv4_code_bits(make_float2(q(bf16lo_to_f32(word[k])), q(bf16hi_to_f32(word[k]))));
-      codes = kv4_pack(c);
+      c0 = kv4_codes8_tiny(val[n][0], s);
+      c1 = kv4_codes8_tiny(val[n][1], s);
     }
-    // V: the thread's two units (4 codes each) lie d / 32 half-words apart; lanes of neighbouring groups trade
-    // halves so that each stores one word.
-    const uint32_t give = (w & 1) ? codes & 0xffffu : codes >> 16;
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 4);
+    if (which == 1) {
+      // Lanes of neighbouring groups trade the codes that fall to the other.
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, (w & 1) ? c0 : c1, 2);
+      const uint32_t lo = (w & 1) ? got : c0, hi = (w & 1) ? c1 : got;
+      c0 = __byte_perm(lo, hi, 0x5410);
+      c1 = __byte_perm(lo, hi, 0x7632);
+    }
     if (dst[n] < 0) continue;
     uint32_t* row = reinterpret_cast<uint32_t*>(out + dst[n] * (D / 2));
-    if (which == 0)
-      row[u * NG + w] = codes;
-    else if (w & 1)
-      row[((2 * u + 1) * NG + w - 1) / 2] = got | (codes & 0xffff0000u);
-    else
-      row[(2 * u * NG + w) / 2] = (codes & 0xffffu) | (got << 16);
-    if (u == 0) steps[dst[n] * NG + w] = step;
+    row[at0] = c0;
+    row[at1] = c1;
+    if (h == 0) steps[dst[n] * NG + w] = step;
   }
 }
 
 template <int D, int R>
 __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const Kv4RowsParams p) {
-  constexpr int TPR = D / 8;
+  constexpr int TPR = D / 16;
   constexpr int NG = D / kKv4Group;
   const int which = blockIdx.y;
   const uint8_t* in = which ? p.codes[1] : p.codes[0];
@@ -179,10 +203,11 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const Kv4RowsParams p)
   __nv_bfloat16* out = which ? p.out[1] : p.out[0];
   const unsigned r0 = blockIdx.x * (256u / TPR * R) + threadIdx.x / TPR;
   const int i = threadIdx.x % TPR;
-  const int w = i / 4, u = i % 4;
-  const int at = which == 0 ? u * NG + w : ((w & 1) ? ((2 * u + 1) * NG + w - 1) / 2 : (2 * u * NG + w) / 2);
+  const int w = i / 2, h = i % 2;
+  const int at0 = which == 0 ? 2 * h * NG + w : ((4 * h + 2 * (w & 1)) * NG + (w & ~1)) / 2;  // as in the write
+  const int at1 = at0 + (which == 0 ? NG : NG / 2);
   bool live[R];
-  uint32_t word[R];
+  uint32_t word[R][2];
   float st[R];
   Kv4Walk walk(p, r0);
 #pragma unroll
@@ -190,30 +215,40 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const Kv4RowsParams p)
     if (n > 0) walk.advance(256 / TPR);
     const long long src = walk.row();
     live[n] = src >= 0;
-    word[n] = 0;
+    word[n][0] = word[n][1] = 0u;
     st[n] = 0.f;
     if (live[n]) {
-      word[n] = reinterpret_cast<const uint32_t*>(in + src * (D / 2))[at];
+      const uint32_t* row = reinterpret_cast<const uint32_t*>(in + src * (D / 2));
+      word[n][0] = row[at0];
+      word[n][1] = row[at1];
       st[n] = __bfloat162float(steps[src * NG + w]);
     }
   }
 #pragma unroll
   for (int n = 0; n < R; ++n) {
-    uint32_t codes = word[n];
-    const uint32_t give = (w & 1) ? codes & 0xffffu : codes >> 16;
-    const uint32_t got = __shfl_xor_sync(0xffffffffu, give, 4);
-    if (!live[n]) continue;
-    if (which == 1) codes = (w & 1) ? got | (codes & 0xffff0000u) : (codes & 0xffffu) | (got << 16);
-    // code - 8 from the low bits of 2^23 + code; step * (code - 8) is exact in fp32; one rounding to bf16.
-    auto with = [&](int k) { return __uint_as_float(0x4b000000u | ((codes >> (4 * k)) & 0xfu)); };
-    uint32_t o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 c = fadd2(make_float2(with(2 * k), with(2 * k + 1)), make_float2(-8388616.f, -8388616.f));
-      const float2 y = fmul2(c, make_float2(st[n], st[n]));
-      o[k] = pack_bf16x2(y.x, y.y);
+    if (__all_sync(0xffffffffu, !live[n])) continue;
+    uint32_t c[2] = {word[n][0], word[n][1]};
+    if (which == 1) {
+      const uint32_t lo = __byte_perm(c[0], c[1], 0x5410), hi = __byte_perm(c[0], c[1], 0x7632);  // even, odd group's
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, (w & 1) ? lo : hi, 2);
+      c[0] = (w & 1) ? got : lo;
+      c[1] = (w & 1) ? hi : got;
     }
-    __stcs(reinterpret_cast<uint4*>(out + (size_t)(r0 + n * (256u / TPR)) * D + 8 * i), make_uint4(o[0], o[1], o[2], o[3]));
+    if (!live[n]) continue;
+    uint4* dst = reinterpret_cast<uint4*>(out + (size_t)(r0 + n * (256u / TPR)) * D + 16 * i);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      // code - 8 from the low bits of 2^23 + code; step * (code - 8) is exact in fp32; one rounding to bf16.
+      auto with = [&](int k) { return __uint_as_float(((c[b] >> (4 * k)) & 0xfu) | 0x4b000000u); };
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 y = fmul2(fadd2(make_float2(with(2 * k), with(2 * k + 1)), make_float2(-8388616.f, -8388616.f)),
+                               make_float2(st[n], st[n]));
+        o[k] = pack_bf16x2(y.x, y.y);
+      }
+      __stcs(dst + b, make_uint4(o[0], o[1], o[2], o[3]));
+    }
   }
 }
 

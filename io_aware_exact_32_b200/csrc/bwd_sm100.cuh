@@ -271,9 +271,24 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
   const int n_per = WIN ? max(0, bwd_last_q_tile(k0, p.Nq, p.Nk, p.window, p.sinks) + 1 - i0) : max(0, nqt - i0);
   const int it0 = cut ? share * p.plen : 0;
   const int n_q = !WIN ? n_per : max(0, min(n_per * p.group, cut ? it0 + p.plen : 0x7fffffff) - it0);
-  // First query row of block `it` of the walk, and its query head.
-  auto q_row = [&](int it) -> int { return (i0 + (WIN ? (it0 + it) % n_per : it)) * 128; };
-  auto q_head = [&](int it) -> int { return WIN ? bh * p.group + (it0 + it) / n_per : bh; };
+  // Where the walk stands: the query block and the head of the next one.
+  struct Walk {
+    int i, end, first, hq;
+    __device__ __forceinline__ int next_row(int& head) {  // first row and head of the next block
+      head = hq;
+      const int row = i * 128;
+      if (++i == end && WIN) {
+        i = first;
+        ++hq;
+      }
+      return row;
+    }
+  };
+  auto walk = [&]() -> Walk {
+    if constexpr (!WIN) return Walk{i0, 0, i0, bh};
+    const int n = n_per > 0 ? n_per : 1;
+    return Walk{i0 + it0 % n, i0 + n, i0, bh * p.group + it0 / n};
+  };
 
   if (threadIdx.x == 0) {
     mbar_init(bar(T::BAR_KV), 1);
@@ -348,8 +363,10 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       }
     };
     bool ok = true;
+    Walk at = walk();
     for (int it = 0; it < n_q; ++it) {
-      const int q0 = q_row(it);
+      int hq;
+      const int q0 = at.next_row(hq);
       [[maybe_unused]] uint32_t braw[2][8];
       if constexpr (EXT) {
         if (has_bias) load_bias(q0, 0, braw[0]);
@@ -360,7 +377,7 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       {
         const int q = q0 + r;
         const bool in = q < p.Nq;
-        const size_t gi = (size_t)q_head(it) * p.Nq + (in ? q : 0);
+        const size_t gi = (size_t)hq * p.Nq + (in ? q : 0);
         float nlse2 = in ? -p.lse[gi] * kLog2e : -INFINITY;
         // EXT: a row the bias hides entirely has LSE = -inf; keep its weights at 0 (a -inf bias
         // entry plus +inf would be NaN).
@@ -576,8 +593,10 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
     // A warp whose wait gave up skips the data steps but still takes the first named barrier of
     // the block, where the group decides whether to go on (so that no warp is left at a barrier
     // the others never reach).
+    Walk at = walk();
     for (int it = 0; it < (DQ ? n_q : 0); ++it) {
-      const int q0 = q_row(it), hq = q_head(it);
+      int hq;
+      const int q0 = at.next_row(hq);
       ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_DQ_FULL), it & 1, abort_flag));
       if constexpr (T::SEP_DQ) {
         uint32_t v[D];
@@ -788,12 +807,14 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       }
       bool ok = true;
       int issued = 0;
+      Walk at = walk();
       for (int it = 0; it < n_q; ++it) {
         const int s = it % T::NS;
         if (!(ok = mbar_wait(bar(T::BAR_QD_EMPTY + s), ((it / T::NS) & 1) ^ 1, abort_flag))) break;
         mbar_arrive_expect_tx(bar(T::BAR_QD_FULL + s), 2 * T::TILE_BYTES);
         const uint32_t dst = sbase + T::OFF_QD + s * 2 * T::TILE_BYTES;
-        const int q0 = q_row(it), hq = q_head(it);
+        int hq;
+        const int q0 = at.next_row(hq);
         for (int b = 0; b < T::NBOX; ++b) {
           tma_load_3d(dst + b * T::BOX_BYTES, &tmQ, bar(T::BAR_QD_FULL + s), 64 * b, q0, hq);
           tma_load_3d(dst + T::TILE_BYTES + b * T::BOX_BYTES, &tmDO, bar(T::BAR_QD_FULL + s), 64 * b, q0, hq);

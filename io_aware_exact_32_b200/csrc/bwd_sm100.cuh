@@ -124,6 +124,7 @@ struct BwdParams {
   // partial dV and dK go to `part` [BH, ns, parts, 2, 128, D] (parts = 1: no cut, written directly).
   int window, sinks, group, ns, parts, plen;
   float* part;
+  int wide;  // dk and dv are 32-byte aligned
 };
 
 // ---------------------------------------------------------------------------------------------
@@ -571,13 +572,19 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
               dst[i] = make_float4(__uint_as_float(v[4 * i]) * mul, __uint_as_float(v[4 * i + 1]) * mul,
                                    __uint_as_float(v[4 * i + 2]) * mul, __uint_as_float(v[4 * i + 3]) * mul);
           } else if (key_ok) {
-            uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
+            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16x2(__uint_as_float(v[8 * i]) * mul, __uint_as_float(v[8 * i + 1]) * mul),
-                                  pack_bf16x2(__uint_as_float(v[8 * i + 2]) * mul, __uint_as_float(v[8 * i + 3]) * mul),
-                                  pack_bf16x2(__uint_as_float(v[8 * i + 4]) * mul, __uint_as_float(v[8 * i + 5]) * mul),
-                                  pack_bf16x2(__uint_as_float(v[8 * i + 6]) * mul, __uint_as_float(v[8 * i + 7]) * mul));
+            for (int i = 0; i < 16; ++i)
+              w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * mul, __uint_as_float(v[2 * i + 1]) * mul);
+            if (WIN && p.wide) {
+              // Whole 32-byte sectors: a warp's stores lie in 32 rows.
+              st_global_v8(out + 32 * c, w);
+              st_global_v8(out + 32 * c + 16, w + 8);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
           }
         }
       }

@@ -417,6 +417,7 @@ fa_status launch_bwd_window(const void* q, const void* k, const void* v, const v
     p.ns = plan.ns;
     p.parts = plan.parts;
     p.plen = plan.plen;
+    p.wide = ((reinterpret_cast<uintptr_t>(dk) | reinterpret_cast<uintptr_t>(dv)) & 31u) == 0 ? 1 : 0;
     p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(dq_acc) + align256((size_t)rows * D * 4));
     // Heads per group as in launch_bwd, with the rows a wave of key tiles touches in place of all of them.
     const int nkt = p.nkt - (plan.parts > 1 ? plan.ns : 0);

@@ -577,21 +577,23 @@ struct DwMeet {
   }
 };
 
-// Merges `parts` > 1 partials, rows row(0 ...), of one (batch, head) by a CTA of 256 threads: 8 warps take every eighth
-// partial each, a lane D / 32 channels.
-template <int D, typename Row>
+// Merges `parts` > 1 partials, rows row(0 ...), of one (batch, head) by a CTA of NW warps: each takes every
+// NW-th partial, a lane D / 32 channels.  NW = 16 where a unit may have more than 16 partials (those of a long sequence
+// then come in one or two rounds of loads), else 4 (a batch's merges then run in one wave; with 16 warps that of
+// B32 H32 took 11 us more).
+template <int D, int NW, typename Row>
 __device__ __forceinline__ void dw_merge(const DecWinParams& p, int parts, Row row) {
   constexpr int PER = D / 32;
-  __shared__ float sm_o[8][D], sm_ml[8][2];
+  __shared__ float sm_o[NW][D], sm_ml[NW][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
   float m = -INFINITY, l = 0.f, acc[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  // A warp's partials warp + 8 i, 32 of them a round: their (m, l) one to a lane, then their rows.
-  for (int c = warp; c < parts; c += 256) {
-    const int n = min(32, (parts - 1 - c) / 8 + 1);
-    const float2 x = lane < n ? ml[row(c + 8 * lane)] : make_float2(-INFINITY, 0.f);
+  // A warp's partials warp + NW i, 32 of them a round: their (m, l) one to a lane, then their rows.
+  for (int c = warp; c < parts; c += 32 * NW) {
+    const int n = min(32, (parts - 1 - c) / NW + 1);
+    const float2 x = lane < n ? ml[row(c + NW * lane)] : make_float2(-INFINITY, 0.f);
     float mx = x.x;
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -606,7 +608,7 @@ __device__ __forceinline__ void dw_merge(const DecWinParams& p, int parts, Row r
 #pragma unroll 8
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
-      const float* src = p.part_o + row(c + 8 * i) * D + lane * PER;
+      const float* src = p.part_o + row(c + NW * i) * D + lane * PER;
       if constexpr (PER == 4) {
         const float4 v = *reinterpret_cast<const float4*>(src);
         acc[0] = fmaf(wi, v.x, acc[0]);
@@ -632,9 +634,9 @@ __device__ __forceinline__ void dw_merge(const DecWinParams& p, int parts, Row r
   if (threadIdx.x >= D) return;
   float mt = -INFINITY, os = 0.f, ls = 0.f;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) mt = fmaxf(mt, sm_ml[w][0]);
+  for (int w = 0; w < NW; ++w) mt = fmaxf(mt, sm_ml[w][0]);
 #pragma unroll
-  for (int w = 0; w < 8; ++w) {
+  for (int w = 0; w < NW; ++w) {
     const float f = ex2_approx(sm_ml[w][0] - mt);
     os = fmaf(f, sm_o[w][threadIdx.x], os);
     ls = fmaf(f, sm_ml[w][1], ls);
@@ -733,12 +735,12 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, false>::CTAS)) fa_de
 
 // One (batch, head) per CTA; launched while the partials' kernel still runs, it waits for that kernel's end.  A head of
 // one part, or without any key, is left alone.
-template <int D>
-__global__ void __launch_bounds__(256) fa_decode_window_merge_kernel(const DecWinParams p) {
+template <int D, int NW>
+__global__ void __launch_bounds__(32 * NW) fa_decode_window_merge_kernel(const DecWinParams p) {
   const int n = dw_keys(p, blockIdx.x / p.H).n, chunk = dw_chunk(p, n);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this grid ends after the partials' does
   const int parts = (n + chunk - 1) / chunk;
-  if (parts > 1) dw_merge<D>(p, parts, [&](int c) { return (size_t)blockIdx.x * p.S + c; });
+  if (parts > 1) dw_merge<D, NW>(p, parts, [&](int c) { return (size_t)blockIdx.x * p.S + c; });
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -747,12 +749,6 @@ __global__ void __launch_bounds__(256) fa_decode_window_merge_kernel(const DecWi
 __device__ __forceinline__ int dw4_steps(int n) {
   constexpr int STEP = DwTile<128, true>::STEP;
   return (n + STEP - 1) / STEP;
-}
-// Steps of sequences 0 .. b - 1, of one unit each; by a whole warp.
-__device__ __forceinline__ int dw4_steps_before(const DecWinParams& p, int b, int lane) {
-  int sum = 0;
-  for (int i = lane; i < b; i += 32) sum += dw4_steps(dw_keys(p, i).n);
-  return __reduce_add_sync(0xffffffffu, sum);
 }
 // Steps per CTA when `total` steps (of all units; below 2^31, checked by the host) are shared out.
 __device__ __forceinline__ int dw4_share(const DecWinParams& p, int total) {
@@ -920,16 +916,22 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, true>::CTAS)) fa_dec
 }
 
 // As fa_decode_window_merge_kernel; a head without any key gets O = 0 and LSE = -inf here.
-template <int D>
-__global__ void __launch_bounds__(256) fa_decode_kv4_merge_kernel(const DecWinParams p) {
+template <int D, int NW>
+__global__ void __launch_bounds__(32 * NW) fa_decode_kv4_merge_kernel(const DecWinParams p) {
   const int lane = threadIdx.x & 31;
   const int b = blockIdx.x / p.H, head = blockIdx.x % p.H;
   const int per_seq = p.Hkv * p.hblocks;
-  const int share = dw4_share(p, dw4_steps_before(p, p.B, lane) * per_seq);
+  int all = 0, before = 0;  // steps of all sequences, of those before b
+  for (int i = lane; i < p.B; i += 32) {
+    const int s = dw4_steps(dw_keys(p, i).n);
+    all += s;
+    before += i < b ? s : 0;
+  }
   const int steps = dw4_steps(dw_keys(p, b).n);
+  const int share = dw4_share(p, __reduce_add_sync(0xffffffffu, all) * per_seq);
   const int in_group = head % p.group;
-  const int unit0 =
-      dw4_steps_before(p, b, lane) * per_seq + (head / p.group * p.hblocks + in_group / kDwHeads) * steps;
+  const int unit0 = __reduce_add_sync(0xffffffffu, before) * per_seq +
+                    (head / p.group * p.hblocks + in_group / kDwHeads) * steps;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this grid ends after the partials' does
   if (steps == 0) {
     if (threadIdx.x < D) p.o[(size_t)blockIdx.x * D + threadIdx.x] = __float2bfloat16(0.f);
@@ -939,7 +941,7 @@ __global__ void __launch_bounds__(256) fa_decode_kv4_merge_kernel(const DecWinPa
   const int c0 = unit0 / share, parts = (unit0 + steps - 1) / share - c0 + 1;
   // The partial of share c0 + i is in its first slot if the share begins inside the unit, else in its last.
   if (parts > 1)
-    dw_merge<D>(p, parts, [&](int i) -> size_t {
+    dw_merge<D, NW>(p, parts, [&](int i) -> size_t {
       return (2 * (size_t)(c0 + i) + ((long long)(c0 + i) * share < unit0 ? 1 : 0)) * kDwHeads + in_group % kDwHeads;
     });
 }

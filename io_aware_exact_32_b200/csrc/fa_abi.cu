@@ -542,15 +542,18 @@ template <int D, bool Q4>
 fa_status launch_decode_window(fa::DecWinParams p, void* ws, cudaStream_t s) {
   const long long BH = (long long)p.B * p.H;
   p.part_o = static_cast<float*>(ws);
+  long long parts;  // partials a unit may have
   if constexpr (Q4) {
     p.grid = decode_kv4_grid(p.B, p.H, p.Hkv, p.Lmax, p.window, p.sinks);
     p.part_ml = p.part_o + (size_t)2 * p.grid * fa::kDwHeads * D;
+    parts = p.grid / decode_window_units(p.B, p.H, p.Hkv) + 2;
     fa::fa_decode_kv4_kernel<D><<<(unsigned)p.grid, 32 * fa::kDwWarps, 0, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
   } else {
     const DwCut cut = decode_window_cut(p.B, p.H, p.Hkv, p.Lmax, p.window, p.sinks);
     p.S = cut.S;
     p.min_chunk = cut.min_chunk;
+    parts = p.S;
     p.part_ml = p.part_o + (size_t)BH * p.S * D;
     const long long blocks = (long long)p.B * p.Hkv * p.hblocks * p.S;
     if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
@@ -564,11 +567,15 @@ fa_status launch_decode_window(fa::DecWinParams p, void* ws, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)BH);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(parts > 16 ? 512 : 128);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  void (*merge)(fa::DecWinParams) = Q4 ? fa::fa_decode_kv4_merge_kernel<D> : fa::fa_decode_window_merge_kernel<D>;
+  void (*merge)(fa::DecWinParams);
+  if constexpr (Q4)
+    merge = parts > 16 ? fa::fa_decode_kv4_merge_kernel<D, 16> : fa::fa_decode_kv4_merge_kernel<D, 4>;
+  else
+    merge = parts > 16 ? fa::fa_decode_window_merge_kernel<D, 16> : fa::fa_decode_window_merge_kernel<D, 4>;
   return cudaLaunchKernelEx(&cfg, merge, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -252,7 +252,10 @@ fa_status launch_fwd(const void* q, const void* k, const void* v, void* o, float
   if (items > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const long long blocks = p.tiles == 2 ? (items < sms ? items : sms) : items;
   // The kernel counts K/V loads per CTA in 32-bit integers.
-  const long long loads_per_cta = ((items + blocks - 1) / blocks) * 2LL * ((Nk + 127) / 128);
+  long long tiles_per_item = (Nk + 127) / 128;
+  if constexpr (WIN)  // the sink tiles, and a window and two row tiles' worth of keys
+    tiles_per_item = std::min<long long>(tiles_per_item, (win->sinks + 127) / 128 + (win->window + 126) / 128 + 3);
+  const long long loads_per_cta = ((items + blocks - 1) / blocks) * 2LL * tiles_per_item;
   if (loads_per_cta > (1LL << 30)) return FA_ERR_UNSUPPORTED;
   CUtensorMap mb;
   if (!ext_bias_map(&mb, ext, Nq, Nk)) return FA_ERR_CUDA;

@@ -485,3 +485,81 @@ def test_generation_together():
         r = Q.decode(pq, kc, ks, vc, vs, lens, W, S, 1 / math.sqrt(d))
         _within(out[:, :, 0], r["o"], r["o_bound"], f"token {i}")
     assert fa.fa_get_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q4", [False, True])
+def test_two_streams_at_once(q4):
+    """Overlapping calls with workspaces of their own."""
+    cases = [_case(4, 8, 2, 3000, 128, [3000, 1, 2999, 700], seed=30 + i) for i in range(2)]
+    want = [_run_decode(q4, c, 2500, 4) for c in cases]
+    args, outs, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for q, k, v, n in cases:
+        kv = (k.to(gc.DEV), v.to(gc.DEV))
+        if q4:
+            cache = fa.kv4_cache(4, 2, 3000, 128, gc.DEV)
+            fa.fa_kv4_write(*kv, cache)
+            kv = (cache,)
+        args.append((q.to(gc.DEV), *kv, n.to(gc.DEV), 2500, 4))
+    torch.cuda.synchronize()
+    f = fa.decode_kv4 if q4 else fa.decode_window
+    for _ in range(5):
+        outs = []
+        for a, s in zip(args, streams):
+            with torch.cuda.stream(s):
+                outs.append(f(*a))
+    torch.cuda.synchronize()
+    for got, ref in zip(outs, want):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("q4", [False, True])
+def test_lse_is_optional(q4):
+    q, k, v, n = _case(2, 4, 2, 400, 64, [400, 0], seed=33)
+    ref = _run_decode(q4, (q, k, v, n), 300, 2)
+    o = torch.full((2, 4, 1, 64), 9.0, dtype=torch.bfloat16, device=gc.DEV)
+    ws = torch.empty(fa.fa_decode_window_workspace_size(2, 4, 2, 400, 64, 300, 2), dtype=torch.uint8, device=gc.DEV)
+    kd, vd = k.to(gc.DEV), v.to(gc.DEV)
+    if q4:
+        cache = fa.kv4_cache(2, 2, 400, 64, gc.DEV)
+        fa.fa_kv4_write(kd, vd, cache)
+        fa.fa_decode_kv4(q.to(gc.DEV), cache, n.to(gc.DEV), 300, 2, o, None, ws)
+    else:
+        fa.fa_decode_window(q.to(gc.DEV), kd, vd, n.to(gc.DEV), 300, 2, o, None, ws)
+    assert torch.equal(o, ref[0])
+
+
+@pytest.mark.gpu
+def test_caches_beyond_32_bit_offsets():
+    """A cache of more than 2^32 bytes (bf16) and 2^31 codes (4 bits): rows at its end are written and attended to."""
+    Hkv, Lmax, d, W, S = 3, 1 << 23, 128, 90, 3
+    lens = [Lmax - 1]
+    q = _bf(1, 6, 1, d, seed=40)
+    rows = torch.cat([torch.arange(S), torch.arange(Lmax - 1 - W, Lmax - 1)])
+    k, v = _bf(1, Hkv, rows.numel(), d, seed=41), _bf(1, Hkv, rows.numel(), d, seed=42)
+    scale = 1 / math.sqrt(d)
+    n = torch.tensor(lens, dtype=torch.int32, device=gc.DEV)
+    kc = torch.empty(1, Hkv, Lmax, d, dtype=torch.bfloat16, device=gc.DEV)
+    vc = torch.empty_like(kc)
+    at = rows.to(gc.DEV)
+    kc[:, :, at], vc[:, :, at] = k.to(gc.DEV), v.to(gc.DEV)
+    assert kc.numel() * 2 > 1 << 32
+    o, lse = fa.decode_window(q.to(gc.DEV), kc, vc, n, W, S, scale=scale)
+    r = OW.decode(_np(q)[:, :, 0], _np(k), _np(v), [rows.numel()], rows.numel(), 0, scale)
+    _within(o[:, :, 0], r["o"], r["o_bound"], "O")
+    del kc, vc
+    cache = fa.KV4Cache(*(torch.empty(1, Hkv, Lmax, m, dtype=t, device=gc.DEV)
+                          for m, t in ((d // 2, torch.uint8), (d // 32, torch.bfloat16)) * 2))
+    for first, count in ((0, S), (Lmax - 1 - W, W)):
+        part = slice(0, S) if first == 0 else slice(S, S + W)
+        start = torch.tensor([first], dtype=torch.int32, device=gc.DEV)
+        fa.fa_kv4_write(k[:, :, part].contiguous().to(gc.DEV), v[:, :, part].contiguous().to(gc.DEV), cache, start)
+    o, lse = fa.decode_kv4(q.to(gc.DEV), cache, n, W, S, scale=scale)
+    (kq, ks), (vq, vs) = Q.quantise(_np(k)), Q.quantise(_np(v))
+    r = Q.decode(_np(q)[:, :, 0], kq, ks, vq, vs, [rows.numel()], rows.numel(), 0, scale)
+    _within(o[:, :, 0], r["o"], r["o_bound"], "O, 4 bits")
+    _within(lse, r["lse"], r["lse_bound"], "LSE, 4 bits")
+    kr, _ = fa.kv4_read(cache, W, torch.tensor([Lmax - 1 - W], dtype=torch.int32, device=gc.DEV))
+    want = Q.values(kq, ks)[:, :, S:]
+    assert np.array_equal(Q.bf16_bits(_np(kr)) & 0x7FFF, Q.bf16_bits(want) & 0x7FFF)

@@ -282,3 +282,61 @@ def test_other_stream_and_graph_replay():
     torch.cuda.synchronize()
     for a, b in zip((o, lse, g[1], g[2]), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_at_any_16_byte_offset(d):
+    """o, dk and dv that are 16- but not 32-byte aligned take other stores: the same bits."""
+    q, k, v, do = gc.to_dev(*_inputs(1, 4, 2, 300, 300, d, seed=7))
+    W, S = 90, 3
+    o, lse = fa.attention_forward_window(q, k, v, W, S)
+    g = fa.attention_backward_window(q, k, v, o, lse, do, W, S)
+
+    def shifted(t):
+        buf = torch.zeros(t.numel() + 16, dtype=t.dtype, device=t.device)
+        x = buf[8:8 + t.numel()].view(t.shape)
+        assert x.data_ptr() % 32 == 16
+        return x
+
+    o2, g2 = shifted(o), [shifted(t) for t in (q, k, v)]
+    fa.fa_fwd_window(q, k, v, o2, lse, W, S)
+    ws = torch.empty(fa.fa_bwd_window_workspace_size(1, 4, 2, 300, 300, d, W, S), dtype=torch.uint8, device=gc.DEV)
+    fa.fa_bwd_window(q, k, v, o2, do, lse, *g2, ws, W, S)
+    assert torch.equal(o, o2) and torch.equal(g[1], g2[1]) and torch.equal(g[2], g2[2])
+
+
+@pytest.mark.gpu
+def test_window_larger_than_any_sequence():
+    q, k, v, _ = gc.to_dev(*_inputs(1, 2, 1, 150, 200, 64, seed=8))
+    a = fa.attention_forward_window(q, k, v, 1 << 40, 1 << 40)
+    b = fa.attention_forward_window(q, k, v, 200)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,Hkv,d,sinks", [(16, 16, 128, 4), (16, 4, 128, 40), (16, 16, 64, 0), (16, 2, 64, 4)])
+def test_waits_give_up_and_the_device_stays_usable(H, Hkv, d, sinks):
+    """With the limit of the kernels' waits lowered, a healthy forward or backward gives up, reports it, and the next
+    call on the device gives the results of before."""
+    x = gc.to_dev(*_inputs(1, H, Hkv, 4096, 4096, d, seed=10))
+    o, lse = fa.attention_forward_window(*x[:3], 500, sinks)
+    g = fa.attention_backward_window(*x[:3], o, lse, x[3], 500, sinks)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_error() == 0
+    for call in (lambda: fa.attention_forward_window(*x[:3], 500, sinks),
+                 lambda: fa.attention_backward_window(*x[:3], o, lse, x[3], 500, sinks)):
+        fa.fa_debug_set_wait_limit(300)
+        try:
+            call()
+            torch.cuda.synchronize()
+            status = fa.fa_get_device_error()
+        finally:
+            fa.fa_debug_set_wait_limit(0)
+        assert status == 6, status
+    o2, lse2 = fa.attention_forward_window(*x[:3], 500, sinks)
+    g2 = fa.attention_backward_window(*x[:3], o2, lse2, x[3], 500, sinks)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_error() == 0
+    for a, b in zip((o, lse) + g[1:], (o2, lse2) + g2[1:]):
+        assert torch.equal(a, b)

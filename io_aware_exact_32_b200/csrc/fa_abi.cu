@@ -422,11 +422,13 @@ fa_status launch_bwd_window(const void* q, const void* k, const void* v, const v
     p.plen = plan.plen;
     p.wide = ((reinterpret_cast<uintptr_t>(dk) | reinterpret_cast<uintptr_t>(dv)) & 31u) == 0 ? 1 : 0;
     p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(dq_acc) + align256((size_t)rows * D * 4));
-    // Heads per group as in launch_bwd, with the rows a wave of key tiles touches in place of all of them.
     const int nkt = p.nkt - (plan.parts > 1 ? plan.ns : 0);
+    // Heads per group as in launch_bwd, with the rows that a key tile's walk touches in place of all of them and one
+    // query head per key/value head (the walks take the heads that share one in turn): about 64 MB of Q, dO and dQ
+    // accumulator.  B4 H16/4 N4096 window 1024: 526 us with a quarter of the heads in a group, 494 with all.
     {
-      const long long per_head = 8LL * std::min<long long>(Nq, (long long)win.window + 128) * D * win.group;
-      long long g = (32LL << 20) / per_head;
+      const long long per_head = 8LL * std::min<long long>(Nq, (long long)win.window + 128) * D;
+      long long g = (64LL << 20) / per_head;
       const long long fill = nkt > 0 ? (num_sms() + nkt - 1) / nkt : 1;
       g = std::max<long long>(1, std::max(g, fill));
       p.hgroup = (int)std::min<long long>(g, kvBH);

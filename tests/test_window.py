@@ -189,6 +189,13 @@ SHAPES = [  # B, H, Hkv, Nq, Nk, d, window, sinks
     (1, 2, 1, 500, 100, 128, 128, 0),      # whole tiles of rows see nothing
     (1, 1, 1, 1300, 1300, 128, 200, 260),
     (1, 8, 1, 200, 200, 64, 33, 5),        # one key/value head for all
+    (2, 6, 3, 333, 333, 128, 70, 8),
+    (1, 2, 2, 200, 500, 128, 64, 2),       # a chunk that lies beyond the sinks' windows altogether
+    (1, 2, 1, 500, 300, 64, 90, 8),        # rows that see nothing, then sinks in and out of their windows
+    (1, 2, 1, 300, 300, 128, 299, 1),      # one row beyond the sink's window
+    (1, 2, 1, 256, 256, 64, 5, 8),         # sinks that leave the window one by one
+    (1, 4, 2, 700, 700, 64, 40, 32),       # the widest narrow sink tile
+    (1, 4, 2, 700, 700, 128, 40, 33),      # the first wide one
     (1, 10, 2, 130, 390, 64, 300, 64),     # groups of five
     (3, 1, 1, 1, 700, 128, 256, 4),        # one query
 ]

@@ -233,7 +233,11 @@ __device__ __forceinline__ void bwd_issue_ss_kmajor(uint32_t tmem_d, uint32_t a_
 // bias, dV uses the dropped and rescaled weights P o Z, and dS = P o (dP o Z - D).
 // WIN: sliding window with sinks, key/value heads shared by p.group query heads.  A CTA owns one key tile
 // of one key/value head and visits, head by head, the query blocks that see it, so dK and dV sum over the
-// sharing heads on chip.
+// sharing heads on chip.  P and dS go to the matrix instructions in bf16, as without a window (an entry off
+// by at most 2^-9 of itself); with the bf16 O that D comes from, dQ, dK and dV end 2.4e-3 to 2.6e-3 off in
+// norm, where rounding exact gradients to bf16 costs 1.7e-3.  What bounds it: the P/dS chain of each block
+// pair.  Measured, of visible pairs only: B4 H16/4 N4096 d128 window 1024 553 us (546 TFLOP/s, with the
+// preprocessing and the dQ conversion), B1 H16 N16301 d64 window 777 385 us (331 TFLOP/s).
 template <int D, bool DQ = true, bool EXT = false, bool WIN = false>
 __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
     fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,

@@ -13,8 +13,9 @@
 // Both kernels only move bytes (2 d one way, 9 d / 16 the other), but at 6.5 TB/s an SM has 4 instructions a clock for
 // 17 channels: a thread takes 16 channels of a row (two lanes a group), so that what is done once a row, a group or a
 // thread is shared by as many channels as its registers hold, and packed fp32 pairs do the arithmetic.  With 8
-// channels a thread the prompt of the measurements took 39 us, write and read back.  Each row is read and written in
-// whole 32-byte sectors.
+// channels a thread a prompt of B4 H8 T2048..4096 d128 took 39 us, write and read back; so it takes 32 to 34 us (each
+// way about 17 us; the issue slots are 63 to 65% and the ALU 52 to 62% busy).  Each row is read and written in whole
+// 32-byte sectors.
 #pragma once
 
 #include "sm100_ptx.cuh"
@@ -127,7 +128,8 @@ __device__ __noinline__ uint32_t kv4_codes8_tiny(uint4 v, float step) {
   return kv4_pack(c);
 }
 
-// R rows per thread, whose loads are in flight together: 2 where that still leaves every SM two blocks, else 1.
+// R rows per thread, whose loads are in flight together: 2 where that still leaves every SM two blocks, else 1 (4 rows:
+// 63 registers, the prompt above 35.5 us).
 template <int D, int R>
 __global__ void __launch_bounds__(256) fa_kv4_write_kernel(const Kv4RowsParams p) {
   constexpr int TPR = D / 16;  // threads per row

@@ -119,10 +119,13 @@ struct BwdParams {
   int H;
   DropoutCfg drop;
   // Sliding-window instantiation only (visibility as in FwdParams).  BH counts key/value heads here, each
-  // shared by `group` query heads; the first ns key tiles hold the sink keys, which every later query
-  // sees: their query blocks are cut into `parts` shares of plen blocks, one CTA each, whose fp32
-  // partial dV and dK go to `part` [BH, ns, parts, 2, 128, D] (parts = 1: no cut, written directly).
-  int window, sinks, group, ns, parts, plen;
+  // shared by `group` query heads.  A key tile's walk over its query blocks may be cut into shares of
+  // consecutive blocks, one CTA each, whose fp32 partial dV and dK go to `part` (bwd_share_slot):
+  //  * the first ns tiles, which hold the sink keys that every later query sees, into `parts` shares of
+  //    plen blocks;
+  //  * every other tile into rparts equal shares, where there are few tiles.
+  // parts, rparts = 1: no cut, written directly.  (parts = 1: the first ns tiles count among the others.)
+  int window, sinks, group, ns, parts, plen, rparts;
   float* part;
   int wide;  // dk and dv are 32-byte aligned
 };
@@ -188,31 +191,41 @@ __device__ __forceinline__ int bwd_last_q_tile(int k0, int Nq, int Nk, int windo
   return qmax < 0 ? -1 : min(last, qmax / 128);
 }
 
-// Window backward: dV, dK of the sink tiles = the sums of their shares' partials, added in share order.
-// One thread per 4 channels of a key.
+// Window backward: where the partial sums of a cut key tile's first share lie in `part`, in units of
+// [2 (dV, dK), 128, D]; its other shares follow.
+__device__ __forceinline__ size_t bwd_share_slot(int BH, int nkt, int ns, int parts, int rparts, int bh, int jt) {
+  const int jt0 = parts > 1 ? ns : 0;
+  if (jt < jt0) return ((size_t)bh * ns + jt) * parts;
+  return (size_t)BH * jt0 * parts + ((size_t)bh * (nkt - jt0) + jt - jt0) * rparts;
+}
+
+// Window backward: dV, dK of the cut key tiles = the sums of their shares' partials, added in share order.
+// One thread per 4 channels of a key; the first nj tiles of every head.
 template <int D>
-__global__ void __launch_bounds__(256) fa_bwd_sink_reduce_kernel(const float* __restrict__ part,
-                                                                 __nv_bfloat16* __restrict__ dk,
-                                                                 __nv_bfloat16* __restrict__ dv, int BH, int Nk, int ns,
-                                                                 int parts) {
+__global__ void __launch_bounds__(256) fa_bwd_share_reduce_kernel(const float* __restrict__ part,
+                                                                  __nv_bfloat16* __restrict__ dk,
+                                                                  __nv_bfloat16* __restrict__ dv, int BH, int Nk,
+                                                                  int nkt, int ns, int parts, int rparts, int nj) {
   const long long i = blockIdx.x * 256ll + threadIdx.x;
   const int c = (int)(i % (D / 4)) * 4;
   const int r = (int)(i / (D / 4) % 128);
   const int which = (int)(i / (D / 4 * 128) % 2);
-  const long long tile = i / (D / 4 * 256);  // bh * ns + jt
-  if (tile >= (long long)BH * ns) return;
-  const int key = (int)(tile % ns) * 128 + r;
+  const long long tile = i / (D / 4 * 256);  // bh * nj + jt
+  if (tile >= (long long)BH * nj) return;
+  const int bh = (int)(tile / nj), jt = (int)(tile % nj);
+  const int key = jt * 128 + r;
   if (key >= Nk) return;
+  const int n = parts > 1 && jt < ns ? parts : rparts;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* src = part + ((tile * parts * 2 + which) * 128 + r) * D + c;
-  for (int s = 0; s < parts; ++s) {
+  const float* src = part + ((bwd_share_slot(BH, nkt, ns, parts, rparts, bh, jt) * 2 + which) * 128 + r) * D + c;
+  for (int s = 0; s < n; ++s) {
     const float4 x = *reinterpret_cast<const float4*>(src + (size_t)s * 256 * D);
     acc.x += x.x;
     acc.y += x.y;
     acc.z += x.z;
     acc.w += x.w;
   }
-  *reinterpret_cast<uint2*>((which ? dk : dv) + ((tile / ns) * Nk + key) * D + c) =
+  *reinterpret_cast<uint2*>((which ? dk : dv) + ((size_t)bh * Nk + key) * D + c) =
       make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 
@@ -238,7 +251,9 @@ __device__ __forceinline__ void bwd_issue_ss_kmajor(uint32_t tmem_d, uint32_t a_
 // norm, where rounding exact gradients to bf16 costs 1.7e-3.  What bounds it: the P/dS chain of each block
 // pair.  Measured, of visible pairs only: B4 H16/4 N4096 d128 window 1024 553 us (546 TFLOP/s, with the
 // preprocessing and the dQ conversion), B1 H16 N16301 d64 window 777 385 us (331 TFLOP/s).
-template <int D, bool DQ = true, bool EXT = false, bool WIN = false>
+// ALL: every key tile's walk is cut (p.rparts > 1); an instantiation of its own, since the tests at run time made the
+// others 0.6 to 1.7% slower.
+template <int D, bool DQ = true, bool EXT = false, bool WIN = false, bool ALL = false>
 __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
     fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
@@ -259,23 +274,26 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
   // blocks sweep them, each block starting at its own query tile.
   // WIN: the cut sink tiles' shares come before everything else (the longest walks first).
   const int n_cut = WIN && p.parts > 1 ? p.BH * p.ns * p.parts : 0;
-  const bool cut = WIN && (int)blockIdx.x < n_cut;
-  const int jt0 = WIN && p.parts > 1 ? p.ns : 0;  // first key tile of the uncut blocks
-  const int bid = cut ? (int)blockIdx.x : (int)blockIdx.x - n_cut;
-  const int nkt = p.nkt - jt0;
-  const int grp = bid / (p.hgroup * (nkt > 0 ? nkt : 1));
+  const bool sink = WIN && (int)blockIdx.x < n_cut;
+  const bool cut = ALL || sink;
+  const int rparts = ALL ? p.rparts : 1;
+  const int jt0 = WIN && p.parts > 1 ? p.ns : 0;  // first of the other key tiles
+  const int bid = sink ? (int)blockIdx.x : (int)blockIdx.x - n_cut;
+  const int per_head = (p.nkt - jt0) * rparts;
+  const int grp = bid / (p.hgroup * (per_head > 0 ? per_head : 1));
   const int gsz = min(p.hgroup, p.BH - grp * p.hgroup);
-  const int r_in = bid - grp * p.hgroup * nkt;
-  const int bh = cut ? bid % p.BH : grp * p.hgroup + r_in % gsz;
-  const int share = cut ? bid / p.BH / p.ns : 0;
-  const int jt = cut ? bid / p.BH % p.ns : jt0 + r_in / gsz;
+  const int r_in = bid - grp * p.hgroup * per_head;
+  const int bh = sink ? bid % p.BH : grp * p.hgroup + r_in % gsz;
+  const int share = sink ? bid / p.BH / p.ns : (ALL ? r_in / gsz % rparts : 0);
+  const int jt = sink ? bid / p.BH % p.ns : jt0 + r_in / gsz / rparts;
   const int k0 = jt * 128;
   const int nqt = (p.Nq + 127) / 128;
   const int i0 = bwd_first_q_tile(k0, p.Nq, p.Nk, p.causal);
   // WIN: the walk is n_per query blocks of each of the group's heads; this CTA takes n_q of them from it0.
   const int n_per = WIN ? max(0, bwd_last_q_tile(k0, p.Nq, p.Nk, p.window, p.sinks) + 1 - i0) : max(0, nqt - i0);
-  const int it0 = cut ? share * p.plen : 0;
-  const int n_q = !WIN ? n_per : max(0, min(n_per * p.group, cut ? it0 + p.plen : 0x7fffffff) - it0);
+  const int slen = sink ? p.plen : (ALL ? (n_per * p.group + rparts - 1) / rparts : 0);
+  const int it0 = cut ? share * slen : 0;
+  const int n_q = !WIN ? n_per : max(0, min(n_per * p.group, cut ? it0 + slen : 0x7fffffff) - it0);
   // Where the walk stands: the query block and the head of the next one.
   struct Walk {
     int i, end, first, hq;
@@ -568,9 +586,9 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
           if (cut) {
-            // A share's part of the sums, fp32, [bh, jt, share, dV / dK, key, channel].
-            float4* dst = reinterpret_cast<float4*>(
-                p.part + (((((size_t)bh * p.ns + jt) * p.parts + share) * 2 + which) * 128 + r) * D + 32 * c);
+            // A share's part of the sums, fp32, [dV / dK, key, channel].
+            const size_t slot = bwd_share_slot(p.BH, p.nkt, p.ns, p.parts, p.rparts, bh, jt) + share;
+            float4* dst = reinterpret_cast<float4*>(p.part + ((slot * 2 + which) * 128 + r) * D + 32 * c);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               dst[i] = make_float4(__uint_as_float(v[4 * i]) * mul, __uint_as_float(v[4 * i + 1]) * mul,

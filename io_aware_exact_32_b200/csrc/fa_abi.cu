@@ -358,25 +358,44 @@ fa_status launch_bwd(const void* q, const void* k, const void* v, const void* o,
   return FA_OK;
 }
 
-// How the window backward cuts the sink tiles' walks over the query blocks, and the fp32 partials it needs.
+// How the window backward cuts its key tiles' walks over the query blocks (see BwdParams), and the fp32 partials it
+// needs.
 struct WinBwdPlan {
-  int ns, parts, plen;
+  int ns, parts, plen, rparts;
   size_t part_bytes;
 };
 
 WinBwdPlan win_bwd_plan(int kvBH, int group, int Nq, int Nk, int d, int window, int sinks) {
-  WinBwdPlan w{(sinks + 127) / 128, 1, 0, 0};
+  WinBwdPlan w{(sinks + 127) / 128, 1, 0, 1, 0};
   const long long nqt = (Nq + 127) / 128, nkt = (Nk + 127) / 128;
-  // Blocks of an ordinary key tile's walk and of a sink tile's; a share is as long as an ordinary walk, or
-  // half of a processor's part of all walks where that is more (148 processors).
+  // Blocks of an ordinary key tile's walk and of a sink tile's, and of all walks.
   const long long reg = (long long)group * std::min<long long>(nqt, (window + 126) / 128 + 1);
   const long long snk = (long long)group * nqt;
-  if (w.ns == 0 || snk <= reg) return w;
-  const long long total = (long long)kvBH * (reg * std::max<long long>(0, nkt - w.ns) + snk * w.ns);
-  const long long plen = std::max<long long>(std::max<long long>(reg, 8), (total + 295) / 296);
-  w.parts = (int)((snk + plen - 1) / plen);
-  w.plen = (int)std::min<long long>(plen, 0x7fffffff);
-  if (w.parts > 1) w.part_bytes = (size_t)kvBH * w.ns * w.parts * 2 * 128 * d * sizeof(float);
+  const long long walks = std::min<long long>(nkt, nqt + (window + 126) / 128);  // ordinary ones
+  const long long total = (long long)kvBH * (reg * std::max<long long>(0, walks - w.ns) + snk * w.ns);
+  // Ordinary walks are cut where that ends the last of them sooner on 148 processors.  In blocks: a walk costs 2.5
+  // besides its own (its loads and its epilogue), a cut 2 and what the partials take.  Where there are more walks
+  // than processors, the last ones leave half a walk idle on average.
+  const long long tiles = walks * kvBH;
+  auto cost = [&](long long parts) {
+    const long long len = (reg + parts - 1) / parts, n = tiles * parts;
+    const double one = (double)len + 2.5;
+    const double all = ((double)reg * tiles + 2.5 * n) / 148;
+    return (n <= 148 ? one : std::max(one, all + 0.5 * one)) + (parts > 1 ? 2 + 0.01 * n : 0);
+  };
+  // Shares of 4 blocks at least; beyond 64 walks a processor the last ones' share of the time is small.
+  if (tiles < 64 * 148)
+    for (int parts = 2; parts <= 32 && reg >= 4 * parts; ++parts)
+      if (cost(parts) < cost(w.rparts)) w.rparts = parts;
+  // A sink tile's share is as long as an ordinary one, or half of a processor's part of all walks where that is more.
+  if (w.ns > 0 && snk > reg) {
+    const long long plen = std::max<long long>(std::max<long long>((reg + w.rparts - 1) / w.rparts, 8), (total + 295) / 296);
+    w.parts = (int)((snk + plen - 1) / plen);
+    w.plen = (int)std::min<long long>(plen, 0x7fffffff);
+  }
+  const long long cut_sinks = w.parts > 1 ? w.ns : 0;
+  const long long slots = cut_sinks * w.parts + (w.rparts > 1 ? (nkt - cut_sinks) * w.rparts : 0);
+  w.part_bytes = (size_t)kvBH * slots * 2 * 128 * d * sizeof(float);
   return w;
 }
 
@@ -398,7 +417,6 @@ fa_status launch_bwd_window(const void* q, const void* k, const void* v, const v
         !make_map_3d(&mdo, dO, D, Nq, BH) || !make_map_3d_f32(&mdq, dq_acc, D, Nq, BH) ||
         !ext_bias_map(&mb, nullptr, Nq, Nk))
       return FA_ERR_CUDA;
-    if (!set_smem(fa::fa_bwd_main_kernel<D, true, false, true>, T::SMEM_BYTES)) return FA_ERR_CUDA;
     fa::BwdParams p;
     set_ext(p, nullptr);
     p.lse = lse;
@@ -420,9 +438,11 @@ fa_status launch_bwd_window(const void* q, const void* k, const void* v, const v
     p.ns = plan.ns;
     p.parts = plan.parts;
     p.plen = plan.plen;
+    p.rparts = plan.rparts;
     p.wide = ((reinterpret_cast<uintptr_t>(dk) | reinterpret_cast<uintptr_t>(dv)) & 31u) == 0 ? 1 : 0;
     p.part = reinterpret_cast<float*>(reinterpret_cast<char*>(dq_acc) + align256((size_t)rows * D * 4));
-    const int nkt = p.nkt - (plan.parts > 1 ? plan.ns : 0);
+    const int cut_sinks = plan.parts > 1 ? plan.ns : 0;
+    const long long nkt = (long long)(p.nkt - cut_sinks) * plan.rparts;  // blocks of a head besides the sinks'
     // Heads per group as in launch_bwd, with the rows that a key tile's walk touches in place of all of them and one
     // query head per key/value head (the walks take the heads that share one in turn): about 64 MB of Q, dO and dQ
     // accumulator.  B4 H16/4 N4096 window 1024: 526 us with a quarter of the heads in a group, 494 with all.
@@ -433,15 +453,20 @@ fa_status launch_bwd_window(const void* q, const void* k, const void* v, const v
       g = std::max<long long>(1, std::max(g, fill));
       p.hgroup = (int)std::min<long long>(g, kvBH);
     }
-    const long long blocks = (long long)nkt * kvBH + (plan.parts > 1 ? (long long)kvBH * plan.ns * plan.parts : 0);
+    const long long blocks = nkt * kvBH + (long long)kvBH * cut_sinks * plan.parts;
     if (blocks > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-    fa::fa_bwd_main_kernel<D, true, false, true><<<(unsigned)blocks, T::THREADS, T::SMEM_BYTES, stream>>>(
-        mq, mk, mv, mdo, mdq, mb, p);
+    const auto kernel = plan.rparts > 1 ? fa::fa_bwd_main_kernel<D, true, false, true, true>
+                                        : fa::fa_bwd_main_kernel<D, true, false, true>;
+    if (!set_smem(kernel, T::SMEM_BYTES)) return FA_ERR_CUDA;
+    kernel<<<(unsigned)blocks, T::THREADS, T::SMEM_BYTES, stream>>>(mq, mk, mv, mdo, mdq, mb, p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
-    if (plan.parts > 1) {
-      const long long n = (long long)kvBH * plan.ns * 256 * (D / 4);
-      fa::fa_bwd_sink_reduce_kernel<D><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(p.part, p.dk, p.dv, kvBH, Nk,
-                                                                                       plan.ns, plan.parts);
+    // The cut tiles: all of them, or the sinks'.
+    const int nj = plan.rparts > 1 ? p.nkt : cut_sinks;
+    if (nj > 0) {
+      const long long n = (long long)kvBH * nj * 256 * (D / 4);
+      if ((n + 255) / 256 > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+      fa::fa_bwd_share_reduce_kernel<D><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
+          p.part, p.dk, p.dv, kvBH, Nk, p.nkt, plan.ns, plan.parts, plan.rparts, nj);
       if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     }
   }

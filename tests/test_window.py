@@ -224,6 +224,32 @@ def test_long_sequence_with_cut_sinks():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,H,Hkv,Nq,Nk,d,window,sinks", [
+    (1, 16, 1, 700, 700, 64, 300, 0),
+    (1, 16, 1, 700, 700, 128, 300, 4),      # sinks cut apart
+    (1, 12, 1, 650, 650, 64, 650, 5),       # sinks among the others
+    (2, 16, 2, 257, 900, 128, 513, 130),    # keys that no query sees; two sink tiles
+    (1, 16, 1, 900, 430, 64, 200, 3),       # queries that see nothing
+    (1, 24, 2, 129, 129, 128, 40, 1),
+])
+def test_few_key_tiles_with_long_walks(B, H, Hkv, Nq, Nk, d, window, sinks):
+    """Every key tile's walk is cut into shares: partials for whole key tiles in the workspace, dK and dV the same bits
+    run to run."""
+    need = fa.fa_bwd_window_workspace_size(B, H, Hkv, Nq, Nk, d, window, sinks)
+    tiles = (need - fa.fa_bwd_workspace_size(B, H, Nq, d)) // (2 * 128 * d * 4)
+    assert tiles >= 2 * B * Hkv * ((Nk + 127) // 128)
+    x = _inputs(B, H, Hkv, Nq, Nk, d, seed=Nq + H)
+    _check(x, window, sinks)
+    q, k, v, do = gc.to_dev(*x)
+    o, lse = fa.attention_forward_window(q, k, v, window, sinks)
+    ws = torch.full((need + 512,), 0xFF, dtype=torch.uint8, device=gc.DEV)  # its contents do not matter: NaN
+    a = fa.attention_backward_window(q, k, v, o, lse, do, window, sinks, workspace=ws[:need])
+    b = fa.attention_backward_window(q, k, v, o, lse, do, window, sinks)
+    assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
+    assert torch.all(ws[need:] == 0xFF)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 def test_equals_the_plain_kernels(d):
     """A window over everything and one key/value head per query head: the same bits as fa_fwd."""

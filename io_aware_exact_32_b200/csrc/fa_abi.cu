@@ -368,25 +368,42 @@ struct WinBwdPlan {
 WinBwdPlan win_bwd_plan(int kvBH, int group, int Nq, int Nk, int d, int window, int sinks) {
   WinBwdPlan w{(sinks + 127) / 128, 1, 0, 1, 0};
   const long long nqt = (Nq + 127) / 128, nkt = (Nk + 127) / 128;
-  // Blocks of an ordinary key tile's walk and of a sink tile's, and of all walks.
+  // Blocks of an ordinary key tile's walk (at most; keys and queries aligned) and of a sink tile's.
   const long long reg = (long long)group * std::min<long long>(nqt, (window + 126) / 128 + 1);
   const long long snk = (long long)group * nqt;
-  const long long walks = std::min<long long>(nkt, nqt + (window + 126) / 128);  // ordinary ones
-  const long long total = (long long)kvBH * (reg * std::max<long long>(0, walks - w.ns) + snk * w.ns);
-  // Ordinary walks are cut where that ends the last of them sooner on 148 processors.  In blocks: a walk costs 2.5
-  // besides its own (its loads and its epilogue), a cut 2 and what the partials take.  Where there are more walks
-  // than processors, the last ones leave half a walk idle on average.
-  const long long tiles = walks * kvBH;
-  auto cost = [&](long long parts) {
-    const long long len = (reg + parts - 1) / parts, n = tiles * parts;
-    const double one = (double)len + 2.5;
-    const double all = ((double)reg * tiles + 2.5 * n) / 148;
-    return (n <= 148 ? one : std::max(one, all + 0.5 * one)) + (parts > 1 ? 2 + 0.01 * n : 0);
-  };
-  // Shares of 4 blocks at least; beyond 64 walks a processor the last ones' share of the time is small.
-  if (tiles < 64 * 148)
-    for (int parts = 2; parts <= 32 && reg >= 4 * parts; ++parts)
-      if (cost(parts) < cost(w.rparts)) w.rparts = parts;
+  // Ordinary walks are cut where that ends the last of them sooner on 148 processors, by a tenth of the time or more.
+  // In blocks (3.4 us each with d = 128): a walk costs 2.5 besides its own (its loads and its epilogue), a cut 2 and
+  // what the partials take; the longest walks come first, and where there are more walks than processors the last ones
+  // leave a quarter of a walk idle.  Best of 2 to 16 shares, measured: B1 H8/1 N4096 window 512 4 (154 -> 69 us),
+  // B1 H8/2 N8192 window 4096 3 (453 -> 340 us), B1 H16/1 N2048 d64 causal 16 (543 -> 64 us; 13 here, 68 us); none at B1 H32/8 N4096
+  // window 1024 (295 us, 312 with 2).  Above 16 walks a processor a cut has nothing to gain.
+  if (nkt * kvBH < 16 * 148) {
+    const long long off = Nk - Nq;
+    long long tiles = 0, longest = 0, sum = 0;
+    for (long long k0 = 0; k0 < Nk; k0 += 128) {
+      const long long q0 = std::max(0LL, k0 - off), q1 = k0 + 126 - off + window;
+      const long long n = q1 < 0 ? 0 : std::min(nqt - 1, q1 / 128) - q0 / 128 + 1;
+      if (n <= 0) continue;
+      ++tiles;
+      longest = std::max(longest, n * group);
+      sum += n * group;
+    }
+    tiles *= kvBH;
+    sum *= kvBH;
+    auto cost = [&](int parts) {
+      const long long n = tiles * parts;
+      const double one = (double)((longest + parts - 1) / parts) + 2.5, all = (sum + 2.5 * n) / 148;
+      return (n <= 148 ? one : std::max(one, all + 0.25 * one)) + (parts > 1 ? 2 + 0.01 * n : 0);
+    };
+    double least = 0.9 * cost(1);
+    for (int parts = 2; parts <= 32 && longest >= 4 * parts; ++parts)
+      if (cost(parts) < least) {
+        least = cost(parts);
+        w.rparts = parts;
+      }
+  }
+  // All walks, roughly.
+  const long long total = (long long)kvBH * (reg * std::max<long long>(0, nkt - w.ns) + snk * w.ns);
   // A sink tile's share is as long as an ordinary one, or half of a processor's part of all walks where that is more.
   if (w.ns > 0 && snk > reg) {
     const long long plen = std::max<long long>(std::max<long long>((reg + w.rparts - 1) / w.rparts, 8), (total + 295) / 296);

@@ -138,6 +138,7 @@ __global__ void __launch_bounds__(256) fa_bwd_preprocess_kernel(const __nv_bfloa
                                                                 const __nv_bfloat16* __restrict__ dout,
                                                                 float* __restrict__ dvec,
                                                                 float* __restrict__ dq_acc, long long rows) {
+  grid_launch_next();
   const long long row = blockIdx.x * 8ll + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
@@ -168,6 +169,7 @@ __global__ void __launch_bounds__(256) fa_bwd_preprocess_kernel(const __nv_bfloa
 // dQ accumulator (already scaled) -> bf16, 8 elements per thread.
 __global__ void __launch_bounds__(256) fa_bwd_dq_convert_kernel(const float* __restrict__ acc,
                                                                 __nv_bfloat16* __restrict__ dq, long long n8) {
+  grid_wait_prior();
   const long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x;
   if (i >= n8) return;
   const float4 a = reinterpret_cast<const float4*>(acc)[2 * i];
@@ -206,6 +208,8 @@ __global__ void __launch_bounds__(256) fa_bwd_share_reduce_kernel(const float* _
                                                                   __nv_bfloat16* __restrict__ dk,
                                                                   __nv_bfloat16* __restrict__ dv, int BH, int Nk,
                                                                   int nkt, int ns, int parts, int rparts, int nj) {
+  grid_launch_next();
+  grid_wait_prior();
   const long long i = blockIdx.x * 256ll + threadIdx.x;
   const int c = (int)(i % (D / 4)) * 4;
   const int r = (int)(i / (D / 4) % 128);
@@ -386,6 +390,7 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       }
     };
     bool ok = true;
+    if constexpr (WIN) grid_wait_prior();  // D and the zeroed accumulator; K, V, Q and dO were there before
     Walk at = walk();
     for (int it = 0; it < n_q; ++it) {
       int hq;
@@ -565,6 +570,7 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       tc_fence_before();
       mbar_arrive(bar(T::BAR_DS_READY));
     }
+    if constexpr (WIN) grid_launch_next();
     // dK, dV epilogue (group 0 owns it; both groups hold the same key rows).
     if (ok && wg == 0 && n_q > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_ACC_DONE), 0, abort_flag));
     if (!ok) {
@@ -622,6 +628,7 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
     // A warp whose wait gave up skips the data steps but still takes the first named barrier of
     // the block, where the group decides whether to go on (so that no warp is left at a barrier
     // the others never reach).
+    if constexpr (WIN) grid_wait_prior();
     Walk at = walk();
     for (int it = 0; it < (DQ ? n_q : 0); ++it) {
       int hq;

@@ -680,7 +680,7 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, false>::CTAS)) fa_de
         p.o[head0 * D + idx] = __float2bfloat16(0.f);
         if (p.lse && idx < nh) p.lse[head0 + idx] = -INFINITY;
       }
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_launch_next();
     return;
   }
   const int i0 = (int)begin, i1 = min(i0 + chunk, keys.n), ns = keys.ns, jump = keys.jump;
@@ -730,7 +730,7 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, false>::CTAS)) fa_de
     if (more) load_v(i + STEP);
   }
   // The merge may be launched: it waits for this grid's end before it reads.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_launch_next();
   meet.put(st, warp, g, t);
   __syncthreads();
   meet.write(p, head0, nh, keys.n <= chunk, [&](int h) { return (head0 + h) * p.S + s_idx; });
@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, false>::CTAS)) fa_de
 template <int D, int NW>
 __global__ void __launch_bounds__(32 * NW) fa_decode_window_merge_kernel(const DecWinParams p) {
   const int n = dw_keys(p, blockIdx.x / p.H).n, chunk = dw_chunk(p, n);
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this grid ends after the partials' does
+  grid_wait_prior();  // by every CTA: this grid ends after the partials' does
   const int parts = (n + chunk - 1) / chunk;
   if (parts > 1) dw_merge<D, NW>(p, parts, [&](int c) { return (size_t)blockIdx.x * p.S + c; });
 }
@@ -915,7 +915,7 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, true>::CTAS)) fa_dec
     }
   }
   // The merge may be launched: it waits for this grid's end before it reads.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_launch_next();
 }
 
 // As fa_decode_window_merge_kernel; a head without any key gets O = 0 and LSE = -inf here.
@@ -935,7 +935,7 @@ __global__ void __launch_bounds__(32 * NW) fa_decode_kv4_merge_kernel(const DecW
   const int in_group = head % p.group;
   const int unit0 = __reduce_add_sync(0xffffffffu, before) * per_seq +
                     (head / p.group * p.hblocks + in_group / kDwHeads) * steps;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // by every CTA: this grid ends after the partials' does
+  grid_wait_prior();  // by every CTA: this grid ends after the partials' does
   if (steps == 0) {
     if (threadIdx.x < D) p.o[(size_t)blockIdx.x * D + threadIdx.x] = __float2bfloat16(0.f);
     if (threadIdx.x == 0 && p.lse) p.lse[blockIdx.x] = -INFINITY;

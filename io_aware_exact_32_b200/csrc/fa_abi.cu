@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <utility>
 
 #include "../../include/fa.h"
 #include "bwd_dq_sm100.cuh"
@@ -120,6 +121,22 @@ bool set_smem(K kernel, int bytes) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
   if (ndone[dev] < 32) done[dev][ndone[dev]++] = reinterpret_cast<const void*>(kernel);
   return true;
+}
+
+// Launches a kernel that may start before the one ahead of it in the stream has ended (it waits for that itself).
+template <typename... P, typename... A>
+bool launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...) == cudaSuccess;
 }
 
 fa_status check_common(int B, int H, int Nq, int Nk, int d, float scale) {
@@ -475,22 +492,23 @@ fa_status launch_bwd_window(const void* q, const void* k, const void* v, const v
     const auto kernel = plan.rparts > 1 ? fa::fa_bwd_main_kernel<D, true, false, true, true>
                                         : fa::fa_bwd_main_kernel<D, true, false, true>;
     if (!set_smem(kernel, T::SMEM_BYTES)) return FA_ERR_CUDA;
-    kernel<<<(unsigned)blocks, T::THREADS, T::SMEM_BYTES, stream>>>(mq, mk, mv, mdo, mdq, mb, p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+    if (!launch_dependent(kernel, (unsigned)blocks, T::THREADS, T::SMEM_BYTES, stream, mq, mk, mv, mdo, mdq, mb, p))
+      return FA_ERR_CUDA;
     // The cut tiles: all of them, or the sinks'.
     const int nj = plan.rparts > 1 ? p.nkt : cut_sinks;
     if (nj > 0) {
       const long long n = (long long)kvBH * nj * 256 * (D / 4);
       if ((n + 255) / 256 > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
-      fa::fa_bwd_share_reduce_kernel<D><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(
-          p.part, p.dk, p.dv, kvBH, Nk, p.nkt, plan.ns, plan.parts, plan.rparts, nj);
-      if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
+      if (!launch_dependent(fa::fa_bwd_share_reduce_kernel<D>, (unsigned)((n + 255) / 256), 256, 0, stream, p.part,
+                            p.dk, p.dv, kvBH, Nk, p.nkt, plan.ns, plan.parts, plan.rparts, nj))
+        return FA_ERR_CUDA;
     }
   }
   const long long n8 = rows * D / 8;
-  fa::fa_bwd_dq_convert_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, stream>>>(
-      dq_acc, static_cast<__nv_bfloat16*>(dq), n8);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_dependent(fa::fa_bwd_dq_convert_kernel, (unsigned)((n8 + 255) / 256), 256, 0, stream, dq_acc,
+                          static_cast<__nv_bfloat16*>(dq), n8)
+             ? FA_OK
+             : FA_ERR_CUDA;
 }
 
 template <int D>
@@ -608,22 +626,13 @@ fa_status launch_decode_window(fa::DecWinParams p, void* ws, cudaStream_t s) {
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_CUDA;
     if (p.S == 1) return FA_OK;
   }
-  // Programmatic dependent launch: the merge's CTAs start while the last of the partials are written.
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)BH);
-  cfg.blockDim = dim3(parts > 16 ? 512 : 128);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  // The merge's CTAs start while the last of the partials are written.
   void (*merge)(fa::DecWinParams);
   if constexpr (Q4)
     merge = parts > 16 ? fa::fa_decode_kv4_merge_kernel<D, 16> : fa::fa_decode_kv4_merge_kernel<D, 4>;
   else
     merge = parts > 16 ? fa::fa_decode_window_merge_kernel<D, 16> : fa::fa_decode_window_merge_kernel<D, 4>;
-  return cudaLaunchKernelEx(&cfg, merge, p) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return launch_dependent(merge, (unsigned)BH, parts > 16 ? 512 : 128, 0, s, p) ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace

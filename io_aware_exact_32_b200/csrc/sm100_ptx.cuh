@@ -144,6 +144,13 @@ __device__ __forceinline__ bool bar_sync_all(uint32_t id, uint32_t n, bool pred)
   return out != 0;
 }
 
+// Programmatic dependent launch.  grid_launch_next: the next kernel of the stream, if launched so, may start once
+// every CTA of this grid has come here or ended.  grid_wait_prior: until the grid before has ended, its writes
+// visible (at once, if this kernel was launched without).  Every CTA of a dependent grid waits, so that a grid's end
+// is also the end of all before it.
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait_prior() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // 32 bytes to global memory in one store (32-byte aligned).
 __device__ __forceinline__ void st_global_v8(void* dst, const uint32_t* w) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),

@@ -216,9 +216,11 @@ struct DwTile<D, true> {
       vs = reinterpret_cast<const uint8_t*>(p.v_steps + (row + g) * NG);
     }
   };
+  // Tile n of the rows from `row` on (n a constant, so that it ends up in the loads' immediate offsets).
   template <typename At>
-  __device__ __forceinline__ void load_k(const Base& base, uint32_t row, int g, int, At at) {
-    const uint8_t *kc = base.k + row * (D / 2), *st = base.ks + row * (2 * NG);
+  __device__ __forceinline__ void load_k(const Base& base, uint32_t row, int n, int g, int, At at) {
+    const uint8_t *kc = base.k + row * (D / 2) + n * (kDwTile * D / 2);
+    const uint8_t *st = base.ks + row * (2 * NG) + n * (kDwTile * 2 * NG);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const long long d = at(g + 8 * r) - g;
@@ -227,8 +229,9 @@ struct DwTile<D, true> {
     }
   }
   template <typename At>
-  __device__ __forceinline__ void load_v(const Base& base, uint32_t row, int g, int t, At at) {
-    const uint8_t *vc = base.v + row * (D / 2), *st = base.vs + row * (2 * NG);
+  __device__ __forceinline__ void load_v(const Base& base, uint32_t row, int n, int g, int t, At at) {
+    const uint8_t *vc = base.v + row * (D / 2) + n * (kDwTile * D / 2);
+    const uint8_t *st = base.vs + row * (2 * NG) + n * (kDwTile * 2 * NG);
 #pragma unroll
     for (int r = 0; r < 4; ++r)
       load_words<NG / 2>(v[r], vc + (long long)(at(2 * t + (r & 1) + 8 * (r >> 1)) - 2 * t) * (D / 2));
@@ -319,26 +322,33 @@ struct DwState<D, true> {
     vtop = ((66u << 7) | 0x7fu) * 0x10001u;
   }
 
-  // Scores of keys g (s[0], s[1]) and g + 8 for heads 2 t and 2 t + 1, in units of fx.
-  __device__ __forceinline__ void scores(const DwTile<D, true>& x, const uint8_t* sm_q, int lane, float (&s)[4]) {
+  // Scores of keys g (s[.][0], s[.][1]) and g + 8 of N tiles for heads 2 t and 2 t + 1, in units of fx.
+  template <int N>
+  __device__ __forceinline__ void scores(const DwTile<D, true> (&x)[N], const uint8_t* sm_q, int lane,
+                                         float (&s)[N][4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] = 0.f;
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
 #pragma unroll
     for (int w = 0; w < NG; ++w) {
-      const uint32_t a = x.k[0][w], b = x.k[1][w];
       uint32_t qf[4];
       lds_words<4>(qf, sm_q + 16 * (32 * w + lane));
       const float2 c0 = *reinterpret_cast<const float2*>(sm_q + NG * 512 + 8 * (32 * w + lane));
-      float d[4] = {c0.x, c0.y, c0.x, c0.y};
-      mma_f16_16816(d, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qf[0], qf[1]);
-      const uint32_t a8 = a >> 8, b8 = b >> 8;
-      mma_f16_16816(d, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, qf[2], qf[3]);
-      const float s0 = (w & 1) ? bf16hi_to_f32(x.ks[0][w / 2]) : bf16lo_to_f32(x.ks[0][w / 2]);
-      const float s1 = (w & 1) ? bf16hi_to_f32(x.ks[1][w / 2]) : bf16lo_to_f32(x.ks[1][w / 2]);
-      s[0] = fmaf(s0, d[0], s[0]);
-      s[1] = fmaf(s0, d[1], s[1]);
-      s[2] = fmaf(s1, d[2], s[2]);
-      s[3] = fmaf(s1, d[3], s[3]);
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        const uint32_t a = x[n].k[0][w], b = x[n].k[1][w];
+        float d[4] = {c0.x, c0.y, c0.x, c0.y};
+        mma_f16_16816(d, a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u, qf[0], qf[1]);
+        const uint32_t a8 = a >> 8, b8 = b >> 8;
+        mma_f16_16816(d, a8 & 0x000f000fu, b8 & 0x000f000fu, a8 & 0x00f000f0u, b8 & 0x00f000f0u, qf[2], qf[3]);
+        const float s0 = (w & 1) ? bf16hi_to_f32(x[n].ks[0][w / 2]) : bf16lo_to_f32(x[n].ks[0][w / 2]);
+        const float s1 = (w & 1) ? bf16hi_to_f32(x[n].ks[1][w / 2]) : bf16lo_to_f32(x[n].ks[1][w / 2]);
+        s[n][0] = fmaf(s0, d[0], s[n][0]);
+        s[n][1] = fmaf(s0, d[1], s[n][1]);
+        s[n][2] = fmaf(s1, d[2], s[n][2]);
+        s[n][3] = fmaf(s1, d[3], s[n][3]);
+      }
     }
   }
 
@@ -845,20 +855,20 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, true>::CTAS)) fa_dec
       if (to_load <= 0) return;
       if (whole()) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[n].load_k(base, row0() + kDwTile * n, g, t, DwRows());
+        for (int n = 0; n < NT; ++n) x[n].load_k(base, row0(), n, g, t, DwRows());
       } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[n].load_k(base, 0, g, t, [&](int r) { return row_of(kDwTile * n + r); });
+        for (int n = 0; n < NT; ++n) x[n].load_k(base, 0, 0, g, t, [&](int r) { return row_of(kDwTile * n + r); });
       }
     };
     auto load_v = [&]() {  // and on to the next step
       if (to_load <= 0) return;
       if (whole()) {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[n].load_v(base, row0() + kDwTile * n, g, t, DwRows());
+        for (int n = 0; n < NT; ++n) x[n].load_v(base, row0(), n, g, t, DwRows());
       } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) x[n].load_v(base, 0, g, t, [&](int r) { return row_of(kDwTile * n + r); });
+        for (int n = 0; n < NT; ++n) x[n].load_v(base, 0, 0, g, t, [&](int r) { return row_of(kDwTile * n + r); });
       }
       if (--to_load > 0 && ++ahead.step == ahead.steps) {
         ahead.next_unit(p);
@@ -881,8 +891,7 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, true>::CTAS)) fa_dec
         st.start(sm_q, lane);
       }
       float s[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) st.scores(x[n], sm_q, lane, s[n]);
+      st.scores(x, sm_q, lane, s);
       load_k();
       const int i = at.step * STEP;
       bool some = true;

@@ -20,7 +20,8 @@
 //         dQ block reuses the dP^T columns once dP^T has been consumed)
 //   SMEM: K_j, V_j (resident), a ring of (Q_i, dO_i) stages, dS^T (bf16, 128-byte swizzle),
 //         and at d = 64 an fp32 staging tile for the dQ block
-//   P/dS warpgroups: one thread per key row, two groups of 64 query columns each: P, dS (the
+//   P/dS warpgroups: one thread per key row, two groups of 64 query columns each (windows with d = 64:
+//              four of 32): P, dS (the
 //              critical path); group 0 also runs the dK/dV epilogue
 //   dQ warpgroup: one thread per query row of the dQ block: read it out of TMEM, release the
 //              columns, then add it into the fp32 accumulator with TMA bulk reduce-adds of a staged
@@ -42,7 +43,8 @@ namespace fa {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-template <int D>
+// GROUPS: P/dS warpgroups, 2 or 4.
+template <int D, int GROUPS = 2>
 struct BwdTraits {
   static_assert(D == 64 || D == 128, "head dim");
   static constexpr bool SEP_DQ = (D == 64);            // dQ block has its own TMEM columns + TMA reduce
@@ -81,19 +83,19 @@ struct BwdTraits {
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t COL_S = 0, COL_DP = 128, COL_DV = 256, COL_DK = 256 + D;
   static constexpr uint32_t COL_DQ = SEP_DQ ? 256 + 2 * D : COL_DP;
-  // Two P/dS warpgroups split the 128 query columns of every key row (the per-row chain of TMEM
-  // loads and exponentials is the critical path); each writes its 64 columns of P^T (32 TMEM
-  // columns of bf16 pairs).  d = 64: P^T has its own 64 columns, so the next block's S^T can be
+  // The P/dS warpgroups split the 128 query columns of every key row (the per-row chain of TMEM
+  // loads and exponentials is the critical path); each writes its columns of P^T (bf16 pairs, half
+  // as many TMEM columns).  d = 64: P^T has its own 64 columns, so the next block's S^T can be
   // computed while this block's P^T still feeds dV.  d = 128: no room; each group's P^T
   // overwrites the start of its own, already read, half of S^T.
   static constexpr bool EARLY = SEP_DQ;
   static constexpr uint32_t COL_P = EARLY ? 256 + 3 * D : COL_S;
-  static constexpr uint32_t P_WG_STRIDE = EARLY ? 32 : 64;  // TMEM columns between the groups' P^T
-  static __host__ __device__ constexpr uint32_t p_col(int kk) {  // P^T columns of K-step kk (16 queries)
-    return COL_P + (uint32_t)(kk / 4) * P_WG_STRIDE + (uint32_t)(kk % 4) * 8;
-  }
-  static constexpr int NCWG = 2;
+  static constexpr int NCWG = GROUPS;
   static constexpr int CW = 128 / NCWG;                 // query columns per P/dS warpgroup
+  static constexpr uint32_t P_WG_STRIDE = EARLY ? CW / 2 : CW;  // TMEM columns between the groups' P^T
+  static __host__ __device__ constexpr uint32_t p_col(int kk) {  // P^T columns of K-step kk (16 queries)
+    return COL_P + (uint32_t)(kk / (CW / 16)) * P_WG_STRIDE + (uint32_t)(kk % (CW / 16)) * 8;
+  }
   static constexpr int WARP_DQ = 4 * NCWG;              // first warp of the dQ warpgroup
   static constexpr int WARP_A = WARP_DQ + 4, WARP_B = WARP_DQ + 5, WARP_TMA = WARP_DQ + 6;
   static constexpr int THREADS = 32 * (WARP_TMA + 1);
@@ -253,17 +255,19 @@ __device__ __forceinline__ void bwd_issue_ss_kmajor(uint32_t tmem_d, uint32_t a_
 // sharing heads on chip.  P and dS go to the matrix instructions in bf16, as without a window (an entry off
 // by at most 2^-9 of itself); with the bf16 O that D comes from, dQ, dK and dV end 2.4e-3 to 2.6e-3 off in
 // norm, where rounding exact gradients to bf16 costs 1.7e-3.  What bounds it: the P/dS chain of each block
-// pair.  Measured, of visible pairs only: B4 H16/4 N4096 d128 window 1024 553 us (546 TFLOP/s, with the
-// preprocessing and the dQ conversion), B1 H16 N16301 d64 window 777 385 us (331 TFLOP/s).
+// pair.  Measured, of visible pairs only: B4 H16/4 N4096 d128 window 1024 535 us (564 TFLOP/s, with the
+// preprocessing and the dQ conversion), B1 H16 N16301 d64 window 777 371 us (344 TFLOP/s).
+// d = 64 has four P/dS groups there (of 32 columns, 80 registers a thread): 380 -> 371 us at the last of these sizes.
+// With d = 128, whose chain goes on through the dQ read-out, they cost 5 to 10%.
 // ALL: every key tile's walk is cut (p.rparts > 1); an instantiation of its own, since the tests at run time made the
 // others 0.6 to 1.7% slower.
 template <int D, bool DQ = true, bool EXT = false, bool WIN = false, bool ALL = false>
-__global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
+__global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS, 1)
     fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                        const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmB,
                        const BwdParams p) {
-  using T = BwdTraits<D>;
+  using T = BwdTraits<D, WIN && D == 64 ? 4 : 2>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -359,7 +363,7 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
 
   if (warp < T::WARP_DQ) {
     // ------------------------------------------------------------------ P / dS warpgroup(s)
-    const int wg = warp >> 2;            // which half of the query columns
+    const int wg = warp >> 2;            // which part of the query columns
     const int cb = wg * T::CW;           // first query column of this group
     const int r = (warp & 3) * 32 + lane;  // key row in the block == TMEM lane
     const int key = k0 + r;
@@ -435,10 +439,10 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       const int cmax = WIN ? (key < p.sinks ? 0x7fffffff : shift - q0 + p.window - 1) : 0x7fffffff;
       const bool masked = __any_sync(0xffffffffu, !key_ok || cmin > cb || (WIN && cmax < cb + T::CW - 1));
       // WIN: the visible query columns of this group as bits.
-      [[maybe_unused]] uint32_t vis[2];
+      [[maybe_unused]] uint32_t vis[T::CW / 32];
       if constexpr (WIN) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < T::CW / 32; ++i) {
           const int c0 = cb + 32 * i;
           const uint32_t upto = cmax < c0 + 31 ? bits_below(cmax + 1 - c0) : 0xffffffffu;
           vis[i] = key_ok ? upto & ~bits_below(cmin - c0) : 0u;
@@ -451,16 +455,17 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       // 16-column chunks, double-buffered: the load of chunk c+1 is issued right after chunk c
       // has arrived and overlaps its arithmetic (a TMEM load wait covers every load in flight).
       constexpr int NCH = T::CW / 16;  // 16-column chunks of this group
-      uint32_t sv[2][16], dpv[2][16];
+      constexpr int NB = T::NCWG == 2 ? 2 : 1;  // buffers
+      uint32_t sv[NB][16], dpv[NB][16];
       tmem_ld32x32b_x16_nowait(lane_addr + T::COL_S + cb, sv[0]);
       tmem_ld32x32b_x16_nowait(lane_addr + T::COL_DP + cb, dpv[0]);
       tmem_wait_ld_2x16(sv[0], dpv[0]);
 #pragma unroll
       for (int ch = 0; ch < NCH; ++ch) {
-        const int cur = ch & 1;
-        if (ch < NCH - 1) {
-          tmem_ld32x32b_x16_nowait(lane_addr + T::COL_S + cb + 16 * (ch + 1), sv[cur ^ 1]);
-          tmem_ld32x32b_x16_nowait(lane_addr + T::COL_DP + cb + 16 * (ch + 1), dpv[cur ^ 1]);
+        const int cur = ch & (NB - 1);
+        if (NB == 2 && ch < NCH - 1) {
+          tmem_ld32x32b_x16_nowait(lane_addr + T::COL_S + cb + 16 * (ch + 1), sv[(cur + 1) % NB]);
+          tmem_ld32x32b_x16_nowait(lane_addr + T::COL_DP + cb + 16 * (ch + 1), dpv[(cur + 1) % NB]);
         }
         uint32_t pk[8], dk[8];
         // EXT: bias and dropout decisions (bit e: column 16 ch + e kept) of this chunk's 16 query
@@ -469,7 +474,7 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
         [[maybe_unused]] uint32_t keepm = 0xffffu;
         if constexpr (EXT) {
           const int qc = q0 + cb + 16 * ch;
-          if (has_bias && ch < NCH - 1) load_bias(q0, ch + 1, braw[cur ^ 1]);
+          if (has_bias && ch < NCH - 1) load_bias(q0, ch + 1, braw[(ch + 1) & 1]);
           if (p.drop.p8 != 0) keepm = dropout_keep_colwise(p.drop, (uint32_t)(qc >> 2), (uint32_t)key, (uint32_t)bh, lane);
         }
 #pragma unroll
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
           float2 s23 = make_float2(__uint_as_float(sv[cur][i + 2]), __uint_as_float(sv[cur][i + 3]));
           if constexpr (EXT) {
             if (has_bias) {
-              const uint32_t b01 = braw[cur][i / 2], b23 = braw[cur][i / 2 + 1];
+              const uint32_t b01 = braw[ch & 1][i / 2], b23 = braw[ch & 1][i / 2 + 1];
               s01 = ffma2(make_float2(__uint_as_float(b01 << 16), __uint_as_float(b01 & 0xffff0000u)), inv2, s01);
               s23 = ffma2(make_float2(__uint_as_float(b23 << 16), __uint_as_float(b23 & 0xffff0000u)), inv2, s23);
             }
@@ -553,7 +558,11 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
                        : "memory");
         }
         if (ch < NCH - 1) {
-          tmem_wait_ld_2x16(sv[cur ^ 1], dpv[cur ^ 1]);
+          if constexpr (NB == 1) {
+            tmem_ld32x32b_x16_nowait(lane_addr + T::COL_S + cb + 16 * (ch + 1), sv[0]);
+            tmem_ld32x32b_x16_nowait(lane_addr + T::COL_DP + cb + 16 * (ch + 1), dpv[0]);
+          }
+          tmem_wait_ld_2x16(sv[(cur + 1) % NB], dpv[(cur + 1) % NB]);
           if (T::EARLY && ch == NCH - 2) {
             // Both blocks of this iteration are now in registers: the issuers may overwrite them.
             tc_fence_before();
@@ -635,14 +644,18 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
       const int q0 = at.next_row(hq);
       ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_DQ_FULL), it & 1, abort_flag));
       if constexpr (T::SEP_DQ) {
-        uint32_t v[D];
-        if (ok) {
-          tc_fence_after();
-          tmem_ld32x32b_x64_nowait(lane_addr + T::COL_DQ, v);
-          tmem_wait_ld_x64(v);
-          // The dQ columns are free as soon as they are in registers.
-          tc_fence_before();
-          mbar_arrive(bar(T::BAR_DQ_FREE));
+        // The dQ columns are free as soon as they are in registers (four P/dS groups leave 80 of them a thread: the
+        // columns are then read and staged by halves).
+        constexpr int PART = T::NCWG == 2 ? D : D / 2;
+        uint32_t v[PART];
+        if constexpr (PART == D) {
+          if (ok) {
+            tc_fence_after();
+            tmem_ld32x32b_x64_nowait(lane_addr + T::COL_DQ, v);
+            tmem_wait_ld_x64(v);
+            tc_fence_before();
+            mbar_arrive(bar(T::BAR_DQ_FREE));
+          }
         }
         // Stage the scaled block as two 32-column fp32 boxes in the 128-byte-swizzle layout (row r
         // at r*128 bytes of each box, 16-byte chunk c at (c ^ r%8)*16: a quarter-warp hits
@@ -653,12 +666,24 @@ __global__ void __launch_bounds__(BwdTraits<D>::THREADS, 1)
           break;
         }
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint32_t addr = stg_row + (c >> 3) * (128 * 128) + (((c & 7) ^ (r & 7)) << 4);
-          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
-                       "f"(__uint_as_float(v[4 * c]) * p.scale), "f"(__uint_as_float(v[4 * c + 1]) * p.scale),
-                       "f"(__uint_as_float(v[4 * c + 2]) * p.scale), "f"(__uint_as_float(v[4 * c + 3]) * p.scale)
-                       : "memory");
+        for (int h = 0; h < D / PART; ++h) {
+          if constexpr (PART != D) {
+            if (h == 0) tc_fence_after();
+            tmem_ld32x32b_x32_wait(lane_addr + T::COL_DQ + PART * h, v);
+            if (h == D / PART - 1) {
+              tc_fence_before();
+              mbar_arrive(bar(T::BAR_DQ_FREE));
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < PART / 4; ++c) {
+            const int cc = c + PART / 4 * h;
+            const uint32_t addr = stg_row + (cc >> 3) * (128 * 128) + (((cc & 7) ^ (r & 7)) << 4);
+            asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                         "f"(__uint_as_float(v[4 * c]) * p.scale), "f"(__uint_as_float(v[4 * c + 1]) * p.scale),
+                         "f"(__uint_as_float(v[4 * c + 2]) * p.scale), "f"(__uint_as_float(v[4 * c + 3]) * p.scale)
+                         : "memory");
+          }
         }
         fence_proxy_async_smem();
         asm volatile("bar.sync 2, 128;" ::: "memory");

@@ -437,7 +437,7 @@ template <int D>
 fa_status launch_bwd_window(const void* q, const void* k, const void* v, const void* o, const void* dO,
                             const float* lse, void* dq, void* dk, void* dv, void* ws, int BH, int Nq, int Nk,
                             float scale, cudaStream_t stream, const WinArgs& win) {
-  using T = fa::BwdTraits<D>;
+  using T = fa::BwdTraits<D, D == 64 ? 4 : 2>;
   const long long rows = (long long)BH * Nq;
   const int kvBH = BH / win.group;
   float* dvec = static_cast<float*>(ws);

@@ -21,8 +21,7 @@
 //   SMEM: K_j, V_j (resident), a ring of (Q_i, dO_i) stages, dS^T (bf16, 128-byte swizzle),
 //         and at d = 64 an fp32 staging tile for the dQ block
 //   P/dS warpgroups: one thread per key row, two groups of 64 query columns each (windows with d = 64:
-//              four of 32): P, dS (the
-//              critical path); group 0 also runs the dK/dV epilogue
+//              four of 32): P, dS (the critical path); group 0 also runs the dK/dV epilogue
 //   dQ warpgroup: one thread per query row of the dQ block: read it out of TMEM, release the
 //              columns, then add it into the fp32 accumulator with TMA bulk reduce-adds of a staged
 //              tile (d = 64: its own staging buffer; d = 128: the block's dO tile once dV has read it)

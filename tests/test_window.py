@@ -317,6 +317,55 @@ def test_other_stream_and_graph_replay():
         assert torch.equal(a, b)
 
 
+def _same_gradients(a, b):
+    """dk and dv the same bits; dq's reduce-adds may meet in another order: its fp32 sums then differ by a few 2^-24 of
+    their terms, and a bf16 result by one step of 2^-7 of itself at most where that crosses a rounding boundary."""
+    assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
+    x, y = a[0].float(), b[0].float()
+    assert torch.all((x - y).abs() <= 2.0 ** -7 * torch.maximum(x.abs(), y.abs()) + 1e-4 * x.abs().max())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,Hkv,N,d,window,sinks", [(4, 2, 900, 64, 200, 3), (16, 1, 700, 128, 300, 4), (8, 8, 300, 128, 50, 0)])
+def test_calls_one_after_another_share_a_workspace(H, Hkv, N, d, window, sinks):
+    """A call's kernels start before the ones ahead of them have ended; the next call's must not disturb them."""
+    xs = [gc.to_dev(*_inputs(1, H, Hkv, N, N, d, seed=s)) for s in (21, 22)]
+    fw = [fa.attention_forward_window(*x[:3], window, sinks) for x in xs]
+    ws = torch.empty(fa.fa_bwd_window_workspace_size(1, H, Hkv, N, N, d, window, sinks), dtype=torch.uint8, device=gc.DEV)
+    want = []
+    for x, (o, lse) in zip(xs, fw):
+        want.append(fa.attention_backward_window(*x[:3], o, lse, x[3], window, sinks))
+        torch.cuda.synchronize()
+    got = [fa.attention_backward_window(*xs[i % 2][:3], *fw[i % 2], xs[i % 2][3], window, sinks, workspace=ws)
+           for i in range(40)]
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        _same_gradients(want[i % 2], g)
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Forward and backward on two streams that overlap, each with its own workspace."""
+    xs = [gc.to_dev(*_inputs(1, 8, 2, 1100, 1100, d, seed=d)) for d in (64, 128)]
+    want = []
+    for x in xs:
+        o, lse = fa.attention_forward_window(*x[:3], 250, 4)
+        want.append((o, lse, fa.attention_backward_window(*x[:3], o, lse, x[3], 250, 4)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(15):
+        for x, s, out in zip(xs, streams, got):
+            with torch.cuda.stream(s):
+                o, lse = fa.attention_forward_window(*x[:3], 250, 4)
+                out.append((o, lse, fa.attention_backward_window(*x[:3], o, lse, x[3], 250, 4)))
+    torch.cuda.synchronize()
+    for w, out in zip(want, got):
+        for o, lse, g in out:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+            _same_gradients(w[2], g)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 128])
 def test_outputs_at_any_16_byte_offset(d):

@@ -373,8 +373,9 @@ FA_API fa_status fa_decode_window(const void* q, const void* k_cache, const void
  *   0 <= T <= 2^24, 1 <= Lmax <= 2^24.
  *
  * fa_decode_kv4: fa_decode_window over such a cache (same workspace query); K and V are the values that
- * the codes stand for.  A non-finite group in a visible row makes the outputs of its key/value head's
- * queries non-finite or meaningless; rows that are not visible are not read.
+ * the codes stand for, of any size: a group's channels keep their accuracy whatever the sizes in other groups, rows and
+ * heads, and the LSE does not depend on V.  A non-finite group in a visible row makes the outputs of its key/value
+ * head's queries non-finite or meaningless; rows that are not visible are not read.
  */
 FA_API fa_status fa_kv4_write(const void* k, const void* v, void* k_codes, void* k_steps, void* v_codes,
                               void* v_steps, const int* starts, const int* lens, int B, int Hkv, int T,

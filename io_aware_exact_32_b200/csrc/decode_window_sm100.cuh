@@ -31,9 +31,19 @@
 //    keys;
 //  * V steps multiply the weights, p * step in fp16 (11 bits; 2^-11 relative), transposed between the two
 //    products by movmatrix.
-// fp16 range: q is scaled by a power of two per head so that its largest entry is in [2^14, 2^15); the weights'
-// base m holds, beside the running maximum, the exponent of the largest V step so far, so p * step stays
-// below 2^14 whatever the steps.  Both are kept until a score outgrows its maximum by 2^8 or a step its bound.
+// Ranges: q is scaled by a power of two per head so that its largest entry is in [2^14, 2^15).  The weights' base m is an
+// integer, kMargin above the maximum it was set at, so that weights are at most 1 until a score outgrows that maximum by
+// 2^kMargin and m moves; the sums l and the LSE see nothing of V.  p * step enters fp16 in units of its own per head and
+// group, a power of two, of which the largest product of the warp's keys so far has 2^kFine or more (what fp16's end
+// takes off any product is then below 2^-28 of that largest one, and of a channel 2^-25, as in an fp32 sum) and no
+// product has 2^16; unit and accumulators change when a step comes that does not fit.  Heads, groups and keys of any
+// sizes so leave each other's bits alone.  Parts hold O, normalised by their own l, so that no sum outgrows the values it
+// averages: V may use all of bf16's range.  One unit for all heads and groups, tied to the largest step, lost a group
+// 2^-28 the size of another; its calls took 51.6 us (B32 H32/8 L1024..8192), 22.6 us (B1 H16/4 L65536) and 39.0 us (the
+// first with d = 64) where these take 52.3, 22.6 and 40.0 (calls in a row), and 56.0 where the rows' sizes are spread as
+// exp(1.5 N(0, 1)) (these 61.6: the general way in refit).  It hangs on the short way for a part's first keys: with a test
+// of every product for the end of fp16's range the first of these took 61 to 67 us (registers), with the general way for
+// the first keys 58.
 // The bf16 form is the same with bf16 products; there p = hi + lo in two bf16 terms (16 bits), since its
 // instruction budget is 3.5 times larger.
 #pragma once
@@ -55,8 +65,8 @@ struct DecWinParams {
   const __nv_bfloat16* k_steps;   // 4-bit cache only
   const __nv_bfloat16* v_steps;
   const int* seqlens;
-  float* part_o;                  // partials: bf16 [B * H, S, D], 4 bits [2 grid, 8, D]
-  float* part_ml;                 // the same without D, 2
+  float* part_o;                  // partials: bf16 O~ [B * H, S, D], 4 bits O [2 grid, 8, D]
+  float* part_ml;                 // their (m, l): the same without D, 2
   __nv_bfloat16* o;               // [B, H, D]
   float* lse;                     // [B, H] or null
   int B, Lmax, H, Hkv, group, hblocks;  // hblocks = ceil(group / 8)
@@ -254,10 +264,12 @@ struct DwState<D, true> {
   static constexpr int Q_BYTES = 32 * (NG * 24 + 8);
   float fx[2];
   float m[2], l[2];      // weights are 2^(score - m), l their sum
-  float m2[2];           // running maximum (kept while no score is 2^8 above it)
-  float top[2];          // scores up to here (in units of fx) need no new m
-  uint32_t vtop;         // V steps up to here (bf16, twice) need no new m
-  float acc[NG][2][4];   // group, channels 4 g + {0, 1} / {2, 3}; the odd channels times 16
+  float top[2];          // scores up to here (m, in units of fx) need no new m
+  uint32_t vtop[NG / 2]; // steps of each group up to here (bf16 pairs) need no new units
+  // Shared memory of the warp, 4 w + t, heads 2 t and 2 t + 1: the factors (1 / unit) of group w's products weight * step
+  // for fp16, and lower bounds of the largest product so far.
+  float4* unit;
+  float acc[NG][2][4];   // group, channels 4 g + {0, 1} / {2, 3}, in those units; the odd channels times 16
 
   // By one warp, q being head g's row (live: there is one).
   static __device__ __forceinline__ void prepare(const DecWinParams& p, const __nv_bfloat16* q, bool live, int g, int t,
@@ -304,7 +316,10 @@ struct DwState<D, true> {
     reinterpret_cast<float2*>(sm_q + NG * 768)[lane] = make_float2(f0, f1);
   }
   // By every warp, once the operands are there.
-  __device__ __forceinline__ void start(const uint8_t* sm_q, int lane) {
+  __device__ __forceinline__ void start(const uint8_t* sm_q, float4* units, int lane) {
+    unit = units;
+    if (lane < 4 * NG) unit[lane] = make_float4(pow2(kFinest), pow2(kFinest), 0.f, 0.f);
+    __syncwarp();
     const float2 f = reinterpret_cast<const float2*>(sm_q + NG * 768)[lane];
     fx[0] = f.x;
     fx[1] = f.y;
@@ -316,10 +331,11 @@ struct DwState<D, true> {
         for (int i = 0; i < 4; ++i) acc[w][b][i] = 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      m[h] = m2[h] = top[h] = -INFINITY;
+      m[h] = top[h] = -INFINITY;
       l[h] = 0.f;
     }
-    vtop = ((66u << 7) | 0x7fu) * 0x10001u;
+#pragma unroll
+    for (int w = 0; w < NG / 2; ++w) vtop[w] = 0u;
   }
 
   // Scores of keys g (s[.][0], s[.][1]) and g + 8 of N tiles for heads 2 t and 2 t + 1, in units of fx.
@@ -352,48 +368,157 @@ struct DwState<D, true> {
     }
   }
 
-  // Moves the bounds before the weights of N tiles are formed: a score 2^8 above its head's maximum does, or a V
-  // step above theirs (never below 2^-60, which keeps the sums in range where V is all but zero).
+  static constexpr int kFinest = 126;  // exponent of the largest factor
+  static constexpr int kMargin = 6;    // m starts this far above the largest score
+  static constexpr int kFine = 3;      // the largest product of a head and group has 2^kFine units or more
+  // 2^e (0 below fp32's normal range).
+  static __device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.f : __uint_as_float((uint32_t)(e + 127) << 23); }
+  static __device__ __forceinline__ int exponent(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }  // x >= 0
+  // Makes room before the weights of N tiles are formed, where a score is above top or a step above vtop.
   template <int N>
-  __device__ __forceinline__ void raise(const DwTile<D, true> (&x)[N], const float (&s)[N][4]) {
-    uint32_t mx = 0u;
+  __device__ __forceinline__ void raise(const DwTile<D, true> (&x)[N], const float (&s)[N][4], int g, int t) {
     float y[2] = {-INFINITY, -INFINITY};
+    uint32_t mx[NG / 2], over = 0u;
+#pragma unroll
+    for (int w = 0; w < NG / 2; ++w) mx[w] = 0u;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
 #pragma unroll
-      for (int w = 0; w < NG / 2; ++w) mx = __vmaxu2(mx, __vmaxu2(x[i].vs[0][w], x[i].vs[1][w]));
+      for (int w = 0; w < NG / 2; ++w) mx[w] = __vmaxu2(mx[w], __vmaxu2(x[i].vs[0][w], x[i].vs[1][w]));
 #pragma unroll
       for (int h = 0; h < 2; ++h) y[h] = fmaxf(y[h], fmaxf(s[i][h], s[i][2 + h]));
     }
-    const bool up = __vmaxu2(mx, vtop) != vtop;
-    if (__any_sync(0xffffffffu, up || y[0] > top[0] || y[1] > top[1])) {
-      mx = __reduce_max_sync(0xffffffffu, max(mx & 0xffffu, mx >> 16));
-      const uint32_t bits = max(vtop & 0xffffu, mx | 0x7fu);  // the largest bf16 of that exponent
-      vtop = bits | (bits << 16);
-      const float e = (float)((int)(bits >> 7) - 126);  // steps stay below 2^e
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+    for (int w = 0; w < NG / 2; ++w) over |= __vmaxu2(mx[w], vtop[w]) ^ vtop[w];
+    if (!__any_sync(0xffffffffu, over != 0u || y[0] > top[0] || y[1] > top[1])) return;
+
+    uint32_t mn[NG / 2];
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) y[h] = fmaxf(y[h], __shfl_xor_sync(0xffffffffu, y[h], off));
-        const float mx2 = fmaxf(m2[h], y[h] * fx[h]);
-        m2[h] = mx2;
-        top[h] = (mx2 + 8.f) / fx[h];
-        const float mn = mx2 - 6.f + e;
-        const float f = m[h] == -INFINITY ? 0.f : ex2_approx(m[h] - mn);
-        m[h] = mn;
-        l[h] *= f;
+    for (int w = 0; w < NG / 2; ++w) {
+      mn[w] = x[0].vs[0][w];
 #pragma unroll
-        for (int w = 0; w < NG; ++w)
+      for (int i = 0; i < N; ++i) mn[w] = __vminu2(mn[w], __vminu2(x[i].vs[0][w], x[i].vs[1][w]));
+    }
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            acc[w][b][h] *= f;
-            acc[w][b][2 + h] *= f;
-          }
+    for (int off = 4; off < 32; off <<= 1) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) y[h] = fmaxf(y[h], __shfl_xor_sync(0xffffffffu, y[h], off));
+#pragma unroll
+      for (int w = 0; w < NG / 2; ++w) mn[w] = __vminu2(mn[w], __shfl_xor_sync(0xffffffffu, mn[w], off));
+    }
+    int up[2];
+    bool moved[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      moved[h] = y[h] > top[h];
+      const float mnew = moved[h] ? fmaxf(m[h], ceilf(y[h] * fx[h]) + kMargin) : m[h];
+      up[h] = m[h] == -INFINITY ? 0 : (int)fminf(mnew - m[h], 512.f);  // from nothing: no sums yet
+      m[h] = mnew;
+      const float q = mnew * rcp_approx(fx[h]);
+      top[h] = fmaf(fabsf(q), -0x1p-20f, q);  // below m / fx: no weight is above 1
+      l[h] *= pow2(-up[h]);
+    }
+    if (vtop[0] == 0u) {
+      // The first keys.  Every head's largest product is 2^-(kMargin + 1) of the smallest step or more: made 2^kFine
+      // units, if that leaves room for weights of 1 at the largest step.
+      constexpr uint32_t room = 15 - kFine - kMargin - 1;  // exponents between them
+      uint32_t vt[NG / 2];
+      over = 0u;
+#pragma unroll
+      for (int w = 0; w < NG / 2; ++w) {
+        vt[w] = (mn[w] & 0x7f807f80u) + ((room << 7) + 0x7fu) * 0x10001u;
+        over |= __vmaxu2(mx[w], vt[w]) ^ vt[w];
+      }
+      if (!__any_sync(0xffffffffu, over != 0u)) {
+        __syncwarp();  // all lanes have read the old ones
+#pragma unroll
+        for (int w = 0; w < NG; ++w) {
+          const int field = (int)(((w & 1) ? mn[w / 2] >> 16 : mn[w / 2] & 0xffffu) >> 7);
+          const float f = pow2(min(kFine + kMargin + 1 + 127 - field, kFinest)), run = pow2(field - 127 - kMargin - 1);
+          if (g == 0) unit[4 * w + t] = make_float4(f, f, run, run);
+        }
+#pragma unroll
+        for (int w = 0; w < NG / 2; ++w) vtop[w] = vt[w];
+        __syncwarp();
+        return;
       }
     }
+    refit(x, s, mx, mn, up, moved, g, t);
   }
 
-  __device__ __forceinline__ void accumulate(const DwTile<D, true>& x, const float (&s)[4]) {
+  // The units in general.  For each head and group a lower bound of the largest product so far is kept; where the steps'
+  // own unit would leave it less than kFine units, the products themselves are looked at.
+  template <int N>
+  __device__ __forceinline__ void refit(const DwTile<D, true> (&x)[N], const float (&s)[N][4], uint32_t (&mx)[NG / 2],
+                                        const uint32_t (&mn)[NG / 2], const int (&up)[2], const bool (&moved)[2], int g,
+                                        int t) {
+#pragma unroll
+    for (int w = 0; w < NG / 2; ++w)
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) mx[w] = __vmaxu2(mx[w], __shfl_xor_sync(0xffffffffu, mx[w], off));
+    float pr[N][4];
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pr[n][i] = ex2_approx(fmaf(s[n][i], fx[i & 1], -m[i & 1]));
+    uint32_t finest[NG / 2];  // exponents + 127 of groups 2 w, 2 w + 1, of all heads
+#pragma unroll
+    for (int w = 0; w < NG; ++w) {
+      const float4 old = unit[4 * w + t];
+      const int field = (int)(((w & 1) ? mx[w / 2] >> 16 : mx[w / 2] & 0xffffu) >> 7);
+      const int least = (int)(((w & 1) ? mn[w / 2] >> 16 : mn[w / 2] & 0xffffu) >> 7);
+      const int own = 14 + 127 - field;
+      int e[2] = {exponent(old.x) + up[0], exponent(old.y) + up[1]};
+      float run[2] = {old.z * pow2(-up[0]), old.w * pow2(-up[1])};
+      bool look = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (moved[h]) run[h] = fmaxf(run[h], pow2(least - 127 - kMargin - 1));
+        look |= own < min(e[h], kFinest) && kFine - exponent(run[h]) > own;
+      }
+      if (__any_sync(0xffffffffu, look)) {
+        float most[2] = {0.f, 0.f};
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t st = x[n].vs[i / 2][w / 2];
+            most[i & 1] = fmaxf(most[i & 1], pr[n][i] * ((w & 1) ? bf16hi_to_f32(st) : bf16lo_to_f32(st)));
+          }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) most[h] = fmaxf(most[h], __shfl_xor_sync(0xffffffffu, most[h], off));
+          run[h] = fmaxf(run[h], most[h]);
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int to = min(min(e[h], kFinest), max(own, kFine - exponent(run[h])));
+        const float c = pow2(to - e[h]);  // (old sums shrink by 2^up, and count 2^up as many of the units that shrank so)
+        e[h] = to;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          acc[w][b][h] *= c;
+          acc[w][b][2 + h] *= c;
+        }
+      }
+      __syncwarp();  // all lanes have read the old ones
+      if (g == 0) unit[4 * w + t] = make_float4(pow2(e[0]), pow2(e[1]), run[0], run[1]);
+      const uint32_t ex = (uint32_t)(max(e[0], e[1]) + 127);
+      finest[w / 2] = (w & 1) ? finest[w / 2] | ex << 16 : ex;
+    }
+#pragma unroll
+    for (int w = 0; w < NG / 2; ++w) {
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) finest[w] = __vmaxu2(finest[w], __shfl_xor_sync(0xffffffffu, finest[w], off));
+      // The largest bf16 below 2^16 units, at most that of exponent 127 (NaN: such steps come here always).
+      vtop[w] = (__vminu2(0x010d010du - finest[w], 0x00fe00feu) << 7) | 0x007f007fu;
+    }
+    __syncwarp();
+  }
+
+  __device__ __forceinline__ void accumulate(const DwTile<D, true>& x, const float (&s)[4], int t) {
     float pr[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) pr[i] = ex2_approx(fmaf(s[i], fx[i & 1], -m[i & 1]));
@@ -405,8 +530,11 @@ struct DwState<D, true> {
     for (int w = 0; w < NG; ++w) {
       const float s0 = (w & 1) ? bf16hi_to_f32(x.vs[0][w / 2]) : bf16lo_to_f32(x.vs[0][w / 2]);
       const float s1 = (w & 1) ? bf16hi_to_f32(x.vs[1][w / 2]) : bf16lo_to_f32(x.vs[1][w / 2]);
-      const uint32_t b0 = movmatrix_trans(pack_f16x2(pr[0] * s0, pr[1] * s0));
-      const uint32_t b1 = movmatrix_trans(pack_f16x2(pr[2] * s1, pr[3] * s1));
+      // The unit first: at most 2^126, and a weight of 0 stays one whatever the step.
+      const float2 f = *reinterpret_cast<const float2*>(unit + 4 * w + t);
+      const float2 p0 = fmul2(make_float2(pr[0], pr[1]), f), p1 = fmul2(make_float2(pr[2], pr[3]), f);
+      const uint32_t b0 = movmatrix_trans(pack_f16x2(p0.x * s0, p0.y * s0));
+      const uint32_t b1 = movmatrix_trans(pack_f16x2(p1.x * s1, p1.y * s1));
       const uint32_t sel = (w & 1) ? 0x7632u : 0x5410u;
       const uint32_t lo = __byte_perm(x.v[0][w / 2], x.v[1][w / 2], sel);
       const uint32_t hi = __byte_perm(x.v[2][w / 2], x.v[3][w / 2], sel);
@@ -416,19 +544,23 @@ struct DwState<D, true> {
     }
   }
 
-  // O~ of this lane's channels: put(channel, head column, value).
+  // O = O~ / l of this lane's channels (l summed over the keys; 0 without a key): put(channel, head column, value).
   template <typename Put>
   __device__ __forceinline__ void finish(int g, int t, Put put) {
+    const float inv[2] = {l[0] == 0.f ? 0.f : rcp_approx(l[0]), l[1] == 0.f ? 0.f : rcp_approx(l[1])};
 #pragma unroll
-    for (int w = 0; w < NG; ++w)
+    for (int w = 0; w < NG; ++w) {
+      const float2 f = *reinterpret_cast<const float2*>(unit + 4 * w + t);
+      const float back[2] = {pow2(-exponent(f.x)), pow2(-exponent(f.y))};
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const int ch = kKv4Group * w + 4 * g + 2 * b;
-          put(ch, 2 * t + h, acc[w][b][h]);
-          put(ch + 1, 2 * t + h, acc[w][b][2 + h] * 0.0625f);
+          put(ch, 2 * t + h, acc[w][b][h] * inv[h] * back[h]);
+          put(ch + 1, 2 * t + h, acc[w][b][2 + h] * 0.0625f * inv[h] * back[h]);
         }
+    }
   }
 };
 
@@ -557,8 +689,8 @@ struct DwMeet {
       }
   }
   // After a barrier: the CTA's result for heads head0 ..., the outputs themselves if this part was the whole unit (done),
-  // else the partials row(h).
-  template <typename Row>
+  // else the partials row(h).  MEANS: the warps have put O, else O~, and the partials are in the same form.
+  template <bool MEANS, typename Row>
   __device__ __forceinline__ void write(const DecWinParams& p, size_t head0, int nh, bool done, Row row) {
     for (int idx = threadIdx.x; idx < nh * D; idx += 32 * kDwWarps) {
       const int h = idx / D, ch = idx % D;
@@ -566,17 +698,30 @@ struct DwMeet {
 #pragma unroll
       for (int w = 0; w < kDwWarps; ++w) mt = fmaxf(mt, ml[w][h][0]);
       float v = 0.f, l = 0.f;
+      if constexpr (MEANS) {  // shares of at most 1 in all, so that no sum outgrows O
+        float f[kDwWarps];
 #pragma unroll
-      for (int w = 0; w < kDwWarps; ++w) {
-        const float lw = ml[w][h][1];
-        if (lw != 0.f) {  // 0: no key (a NaN sum goes on as one)
-          const float f = ex2_approx(ml[w][h][0] - mt);
-          v = fmaf(f, o[w][h][ch], v);
-          l = fmaf(f, lw, l);
+        for (int w = 0; w < kDwWarps; ++w) {
+          const float lw = ml[w][h][1];
+          f[w] = lw != 0.f ? ex2_approx(ml[w][h][0] - mt) * lw : 0.f;  // 0: no key (a NaN sum goes on as one)
+          l += f[w];
+        }
+        const float inv = rcp_approx(l);
+#pragma unroll
+        for (int w = 0; w < kDwWarps; ++w) v = fmaf(f[w] * inv, o[w][h][ch], v);
+      } else {
+#pragma unroll
+        for (int w = 0; w < kDwWarps; ++w) {
+          const float lw = ml[w][h][1];
+          if (lw != 0.f) {  // as above
+            const float f = ex2_approx(ml[w][h][0] - mt);
+            v = fmaf(f, o[w][h][ch], v);
+            l = fmaf(f, lw, l);
+          }
         }
       }
       if (done) {
-        p.o[(head0 + h) * D + ch] = __float2bfloat16(v / l);
+        p.o[(head0 + h) * D + ch] = __float2bfloat16(MEANS ? v : v / l);
         if (ch == 0 && p.lse) p.lse[head0 + h] = (mt + log2f(l)) * 0.6931471805599453f;
       } else {
         const size_t part = row(h);
@@ -593,8 +738,8 @@ struct DwMeet {
 // Merges `parts` > 1 partials, rows row(0 ...), of one (batch, head) by a CTA of NW warps: each takes every
 // NW-th partial, a lane D / 32 channels.  NW = 16 where a unit may have more than 16 partials (those of a long sequence
 // then come in one or two rounds of loads), else 4 (a batch's merges then run in one wave; with 16 warps that of
-// B32 H32 took 11 us more).
-template <int D, int NW, typename Row>
+// B32 H32 took 11 us more).  MEANS: the partials are O, else O~.
+template <int D, int NW, bool MEANS, typename Row>
 __device__ __forceinline__ void dw_merge(const DecWinParams& p, int parts, Row row) {
   constexpr int PER = D / 32;
   __shared__ float sm_o[NW][D], sm_ml[NW][2];
@@ -611,13 +756,25 @@ __device__ __forceinline__ void dw_merge(const DecWinParams& p, int parts, Row r
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     mx = fmaxf(m, mx);
-    const float f = ex2_approx(m - mx);  // 0 at first
+    float f = ex2_approx(m - mx);  // 0 at first
     m = mx;
     l *= f;
+    float w = ex2_approx(x.x - m);
+    if constexpr (MEANS) {  // l is the warp's, acc the mean so far
+      w *= x.y;
+      float sum = w;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      sum += l;
+      const float inv = rcp_approx(sum);
+      f = l * inv;
+      w *= inv;
+      l = sum;
+    } else {
+      l = fmaf(w, x.y, l);  // this lane's part
+    }
 #pragma unroll
     for (int e = 0; e < PER; ++e) acc[e] *= f;
-    const float w = ex2_approx(x.x - m);
-    l = fmaf(w, x.y, l);  // this lane's part
 #pragma unroll 8
     for (int i = 0; i < n; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
@@ -635,8 +792,10 @@ __device__ __forceinline__ void dw_merge(const DecWinParams& p, int parts, Row r
       }
     }
   }
+  if constexpr (!MEANS) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+  }
 #pragma unroll
   for (int e = 0; e < PER; ++e) sm_o[warp][lane * PER + e] = acc[e];
   if (lane == 0) {
@@ -648,13 +807,23 @@ __device__ __forceinline__ void dw_merge(const DecWinParams& p, int parts, Row r
   float mt = -INFINITY, os = 0.f, ls = 0.f;
 #pragma unroll
   for (int w = 0; w < NW; ++w) mt = fmaxf(mt, sm_ml[w][0]);
+  if constexpr (MEANS) {
 #pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    const float f = ex2_approx(sm_ml[w][0] - mt);
-    os = fmaf(f, sm_o[w][threadIdx.x], os);
-    ls = fmaf(f, sm_ml[w][1], ls);
+    for (int w = 0; w < NW; ++w) ls = fmaf(ex2_approx(sm_ml[w][0] - mt), sm_ml[w][1], ls);
+    const float inv = rcp_approx(ls);
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+      os = fmaf(ex2_approx(sm_ml[w][0] - mt) * sm_ml[w][1] * inv, sm_o[w][threadIdx.x], os);
+  } else {
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float f = ex2_approx(sm_ml[w][0] - mt);
+      os = fmaf(f, sm_o[w][threadIdx.x], os);
+      ls = fmaf(f, sm_ml[w][1], ls);
+    }
+    os /= ls;
   }
-  p.o[(size_t)blockIdx.x * D + threadIdx.x] = __float2bfloat16(os / ls);
+  p.o[(size_t)blockIdx.x * D + threadIdx.x] = __float2bfloat16(os);
   if (p.lse && threadIdx.x == 0) p.lse[blockIdx.x] = (mt + log2f(ls)) * 0.6931471805599453f;
 }
 
@@ -743,7 +912,7 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, false>::CTAS)) fa_de
   grid_launch_next();
   meet.put(st, warp, g, t);
   __syncthreads();
-  meet.write(p, head0, nh, keys.n <= chunk, [&](int h) { return (head0 + h) * p.S + s_idx; });
+  meet.template write<false>(p, head0, nh, keys.n <= chunk, [&](int h) { return (head0 + h) * p.S + s_idx; });
 }
 
 // One (batch, head) per CTA; launched while the partials' kernel still runs, it waits for that kernel's end.  A head of
@@ -753,7 +922,7 @@ __global__ void __launch_bounds__(32 * NW) fa_decode_window_merge_kernel(const D
   const int n = dw_keys(p, blockIdx.x / p.H).n, chunk = dw_chunk(p, n);
   grid_wait_prior();  // by every CTA: this grid ends after the partials' does
   const int parts = (n + chunk - 1) / chunk;
-  if (parts > 1) dw_merge<D, NW>(p, parts, [&](int c) { return (size_t)blockIdx.x * p.S + c; });
+  if (parts > 1) dw_merge<D, NW, false>(p, parts, [&](int c) { return (size_t)blockIdx.x * p.S + c; });
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -796,6 +965,7 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, true>::CTAS)) fa_dec
   constexpr int NT = Tile::NT, STEP = Tile::STEP;
   __shared__ DwMeet<D> meet;
   __shared__ __align__(16) uint8_t sm_q[State::Q_BYTES];
+  __shared__ float4 sm_unit[kDwWarps][4 * State::NG];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int per_seq = p.Hkv * p.hblocks;  // units of a sequence
@@ -888,7 +1058,7 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, true>::CTAS)) fa_dec
           State::prepare(p, p.q + (head0 + min(g, nh - 1)) * D, g < nh, g, t, sm_q);
         }
         __syncthreads();  // also: the last segment's states have been read
-        st.start(sm_q, lane);
+        st.start(sm_q, sm_unit[warp], lane);
       }
       float s[NT][4];
       st.scores(x, sm_q, lane, s);
@@ -905,9 +1075,9 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, true>::CTAS)) fa_dec
         some = i + w0 < at.keys.n;
       }
       if (some) {
-        st.raise(x, s);
+        st.raise(x, s, g, t);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) st.accumulate(x[n], s[n]);
+        for (int n = 0; n < NT; ++n) st.accumulate(x[n], s[n], t);
       }
       load_v();
       ++at.step;
@@ -918,7 +1088,7 @@ __global__ void __launch_bounds__(32 * kDwWarps, (DwTile<D, true>::CTAS)) fa_dec
       meet.put(st, warp, g, t);
       __syncthreads();
       const size_t part = (2 * (size_t)blockIdx.x + (seg0 == begin ? 0 : 1)) * kDwHeads;
-      meet.write(p, head0, nh, j + 1 - seg0 == at.steps, [&](int h) { return part + h; });
+      meet.template write<true>(p, head0, nh, j + 1 - seg0 == at.steps, [&](int h) { return part + h; });
       seg0 = j + 1;
       if (j + 1 < end) at.next_unit(p);
     }
@@ -953,7 +1123,7 @@ __global__ void __launch_bounds__(32 * NW) fa_decode_kv4_merge_kernel(const DecW
   const int c0 = unit0 / share, parts = (unit0 + steps - 1) / share - c0 + 1;
   // The partial of share c0 + i is in its first slot if the share begins inside the unit, else in its last.
   if (parts > 1)
-    dw_merge<D, NW>(p, parts, [&](int i) -> size_t {
+    dw_merge<D, NW, true>(p, parts, [&](int i) -> size_t {
       return (2 * (size_t)(c0 + i) + ((long long)(c0 + i) * share < unit0 ? 1 : 0)) * kDwHeads + in_group % kDwHeads;
     });
 }

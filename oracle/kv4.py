@@ -73,8 +73,10 @@ def unpack(stored, which):
 
 def decode(q, k_codes, k_steps, v_codes, v_steps, lengths, window, sinks, scale):
     """Single-token attention over a cache given as codes (one a channel) and step bits; q [B, H, d] float64.  Dict of
-    o, lse and bounds: weights times steps rounded once to fp16 (2^-11 relative, 2^-25 of the largest absolutely),
-    fp32 sums of code products whose offset 8 cancels, the output rounded to bf16 (2^-8)."""
+    o, lse and bounds: weights times steps rounded once to fp16 (2^-11 relative; absolutely, where a product is small, half
+    a subnormal step 2^-25 in units of which the largest product of the head and group has 2^3 or more, for codes up to
+    7: below 2^-25 of that product a key), fp32 sums, the output rounded to bf16 (2^-8).  A group's bound holds nothing
+    of other groups, and the LSE's nothing of V."""
     from . import windowed as W
     k, v = values(k_codes, k_steps), values(v_codes, v_steps)
     B, H, d = q.shape
@@ -96,10 +98,10 @@ def decode(q, k_codes, k_steps, v_codes, v_steps, lengths, window, sinks, scale)
             o = p @ V
             rep = lambda x: np.repeat(x, GROUP, axis=-1)  # noqa: E731
             terms = rep(p @ vs)
-            largest = (p[:, None] * vs).max()
+            largest = rep((p[:, None] * vs).max(axis=0))
             r["o"][b, h] = o
             r["o_bound"][b, h] = 2.0 ** -8 * np.abs(o) + 2.0 ** -10 * (p @ np.abs(V)) + 2.0 ** -12 * 8 * terms + \
-                idx.size * 2.0 ** -28 * largest
+                idx.size * 2.0 ** -25 * largest
             size = scale * (ks @ np.abs(q[b, h]).reshape(-1, GROUP).sum(1) * 15).max()
             r["lse_bound"][b, h] = 2.0 ** -19 * (1 + size + abs(r["lse"][b, h]))
     return r

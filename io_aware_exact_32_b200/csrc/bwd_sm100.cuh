@@ -119,17 +119,25 @@ struct BwdParams {
   int bias_pb, bias_ph;
   int H;
   DropoutCfg drop;
-  // Sliding-window instantiation only (visibility as in FwdParams).  BH counts key/value heads here, each
-  // shared by `group` query heads.  A key tile's walk over its query blocks may be cut into shares of
-  // consecutive blocks, one CTA each, whose fp32 partial dV and dK go to `part` (bwd_share_slot):
-  //  * the first ns tiles, which hold the sink keys that every later query sees, into `parts` shares of
-  //    plen blocks;
-  //  * every other tile into rparts equal shares, where there are few tiles.
-  // parts, rparts = 1: no cut, written directly.  (parts = 1: the first ns tiles count among the others.)
+};
+
+// The sliding-window instantiations' (visibility, and why a type of their own, as in FwdWinParams).  BH counts key/value
+// heads here, each shared by `group` query heads.  A key tile's walk over its query blocks may be cut into shares of
+// consecutive blocks, one CTA each, whose fp32 partial dV and dK go to `part` (bwd_share_slot):
+//  * the first ns tiles, which hold the sink keys that every later query sees, into `parts` shares of
+//    plen blocks;
+//  * every other tile into rparts equal shares, where there are few tiles.
+// parts, rparts = 1: no cut, written directly.  (parts = 1: the first ns tiles count among the others.)
+struct BwdWinParams : BwdParams {
   int window, sinks, group, ns, parts, plen, rparts;
   float* part;
   int wide;  // dk and dv are 32-byte aligned
 };
+// What an instantiation is given.  The plain ones have the window's fields too, unread: ptxas then takes 118 registers
+// for them in place of 128, and their times are 0.5 to 1.5% shorter (B4 H16 N4096 causal d64 621 against 625 us,
+// deterministic 872 against 886).  With them the bias and dropout one spills (d64 bias and dropout 1508 to 1617 us).
+template <bool EXT>
+using BwdMainParams = std::conditional_t<EXT, BwdParams, BwdWinParams>;
 
 // ---------------------------------------------------------------------------------------------
 // D_i = sum_k dO_ik O_ik and dQ accumulator zeroing.  One warp per query row.
@@ -265,7 +273,7 @@ __global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS,
     fa_bwd_main_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                        const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmDO,
                        const __grid_constant__ CUtensorMap tmDQ, const __grid_constant__ CUtensorMap tmB,
-                       const BwdParams p) {
+                       const BwdMainParams<EXT> p) {
   using T = BwdTraits<D, WIN && D == 64 ? 4 : 2>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -279,29 +287,46 @@ __global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS,
   // Blocks run in groups of hgroup heads; inside a group, every key tile of those heads, the
   // heaviest (causal) first.  The group's Q, dO and dQ accumulator then stay in L2 while its
   // blocks sweep them, each block starting at its own query tile.
-  // WIN: the cut sink tiles' shares come before everything else (the longest walks first).
-  const int n_cut = WIN && p.parts > 1 ? p.BH * p.ns * p.parts : 0;
-  const bool sink = WIN && (int)blockIdx.x < n_cut;
-  const bool cut = ALL || sink;
-  const int rparts = ALL ? p.rparts : 1;
-  const int jt0 = WIN && p.parts > 1 ? p.ns : 0;  // first of the other key tiles
-  const int bid = sink ? (int)blockIdx.x : (int)blockIdx.x - n_cut;
-  const int per_head = (p.nkt - jt0) * rparts;
-  const int grp = bid / (p.hgroup * (per_head > 0 ? per_head : 1));
-  const int gsz = min(p.hgroup, p.BH - grp * p.hgroup);
-  const int r_in = bid - grp * p.hgroup * per_head;
-  const int bh = sink ? bid % p.BH : grp * p.hgroup + r_in % gsz;
-  const int share = sink ? bid / p.BH / p.ns : (ALL ? r_in / gsz % rparts : 0);
-  const int jt = sink ? bid / p.BH % p.ns : jt0 + r_in / gsz / rparts;
-  const int k0 = jt * 128;
   const int nqt = (p.Nq + 127) / 128;
-  const int i0 = bwd_first_q_tile(k0, p.Nq, p.Nk, p.causal);
-  // WIN: the walk is n_per query blocks of each of the group's heads; this CTA takes n_q of them from it0.
-  const int n_per = WIN ? max(0, bwd_last_q_tile(k0, p.Nq, p.Nk, p.window, p.sinks) + 1 - i0) : max(0, nqt - i0);
-  const int slen = sink ? p.plen : (ALL ? (n_per * p.group + rparts - 1) / rparts : 0);
-  const int it0 = cut ? share * slen : 0;
-  const int n_q = !WIN ? n_per : max(0, min(n_per * p.group, cut ? it0 + slen : 0x7fffffff) - it0);
-  // Where the walk stands: the query block and the head of the next one.
+  int bh, jt, k0, i0, n_q;  // (key/value) head, key tile and its first key, first query block, blocks
+  [[maybe_unused]] bool cut = ALL;                       // WIN: this walk is a share of one
+  [[maybe_unused]] int share = 0, it0 = 0, n_per = 1;    // WIN: which, its first block, blocks of a head
+  if constexpr (WIN) {
+    // The cut sink tiles' shares come before everything else (the longest walks first).
+    const int n_cut = p.parts > 1 ? p.BH * p.ns * p.parts : 0;
+    const bool sink = (int)blockIdx.x < n_cut;
+    cut = ALL || sink;
+    const int rparts = ALL ? p.rparts : 1;
+    const int jt0 = p.parts > 1 ? p.ns : 0;  // first of the other key tiles
+    const int bid = sink ? (int)blockIdx.x : (int)blockIdx.x - n_cut;
+    const int per_head = (p.nkt - jt0) * rparts;
+    const int grp = bid / (p.hgroup * (per_head > 0 ? per_head : 1));
+    const int gsz = min(p.hgroup, p.BH - grp * p.hgroup);
+    const int r_in = bid - grp * p.hgroup * per_head;
+    bh = sink ? bid % p.BH : grp * p.hgroup + r_in % gsz;
+    share = sink ? bid / p.BH / p.ns : (ALL ? r_in / gsz % rparts : 0);
+    jt = sink ? bid / p.BH % p.ns : jt0 + r_in / gsz / rparts;
+    k0 = jt * 128;
+    i0 = bwd_first_q_tile(k0, p.Nq, p.Nk, p.causal);
+    // The walk is n_per query blocks of each of the group's heads; this CTA takes n_q of them from it0.
+    n_per = max(0, bwd_last_q_tile(k0, p.Nq, p.Nk, p.window, p.sinks) + 1 - i0);
+    const int slen = sink ? p.plen : (ALL ? (n_per * p.group + rparts - 1) / rparts : 0);
+    it0 = cut ? share * slen : 0;
+    n_q = max(0, min(n_per * p.group, cut ? it0 + slen : 0x7fffffff) - it0);
+    n_per = max(1, n_per);
+  } else {
+    const int bid = blockIdx.x;
+    const int grp = bid / (p.hgroup * p.nkt);
+    const int gsz = min(p.hgroup, p.BH - grp * p.hgroup);
+    const int r_in = bid - grp * p.hgroup * p.nkt;
+    bh = grp * p.hgroup + r_in % gsz;
+    jt = r_in / gsz;
+    k0 = jt * 128;
+    i0 = bwd_first_q_tile(k0, p.Nq, p.Nk, p.causal);
+    n_q = max(0, nqt - i0);
+  }
+  // Where the walk stands: the query block and the head of the next one.  (EXT: from the block's number; the counters
+  // cost the bias and dropout kernels up to 2%.)
   struct Walk {
     int i, end, first, hq;
     __device__ __forceinline__ int next_row(int& head) {  // first row and head of the next block
@@ -315,9 +340,13 @@ __global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS,
     }
   };
   auto walk = [&]() -> Walk {
-    if constexpr (!WIN) return Walk{i0, 0, i0, bh};
-    const int n = n_per > 0 ? n_per : 1;
-    return Walk{i0 + it0 % n, i0 + n, i0, bh * p.group + it0 / n};
+    if constexpr (WIN) return Walk{i0 + it0 % n_per, i0 + n_per, i0, bh * p.group + it0 / n_per};
+    return Walk{i0, 0, i0, bh};
+  };
+  auto next_row = [&](Walk& at, int it, int& hq) -> int {
+    if constexpr (!EXT) return at.next_row(hq);
+    hq = bh;
+    return (i0 + it) * 128;
   };
 
   if (threadIdx.x == 0) {
@@ -397,7 +426,7 @@ __global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS,
     Walk at = walk();
     for (int it = 0; it < n_q; ++it) {
       int hq;
-      const int q0 = at.next_row(hq);
+      const int q0 = next_row(at, it, hq);
       [[maybe_unused]] uint32_t braw[2][8];
       if constexpr (EXT) {
         if (has_bias) load_bias(q0, 0, braw[0]);
@@ -435,7 +464,8 @@ __global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS,
       const int cmin = p.causal ? shift - q0 : -1;
       // Masking is needed only where this warp holds a key past Nk or a causally hidden entry.
       // WIN: nor beyond cmax, unless it is a sink.
-      const int cmax = WIN ? (key < p.sinks ? 0x7fffffff : shift - q0 + p.window - 1) : 0x7fffffff;
+      int cmax = 0x7fffffff;
+      if constexpr (WIN) cmax = key < p.sinks ? 0x7fffffff : shift - q0 + p.window - 1;
       const bool masked = __any_sync(0xffffffffu, !key_ok || cmin > cb || (WIN && cmax < cb + T::CW - 1));
       // WIN: the visible query columns of this group as bits.
       [[maybe_unused]] uint32_t vis[T::CW / 32];
@@ -599,28 +629,36 @@ __global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS,
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0u;
           }
-          if (cut) {
-            // A share's part of the sums, fp32, [dV / dK, key, channel].
-            const size_t slot = bwd_share_slot(p.BH, p.nkt, p.ns, p.parts, p.rparts, bh, jt) + share;
-            float4* dst = reinterpret_cast<float4*>(p.part + ((slot * 2 + which) * 128 + r) * D + 32 * c);
+          if constexpr (WIN) {
+            if (cut) {
+              // A share's part of the sums, fp32, [dV / dK, key, channel].
+              const size_t slot = bwd_share_slot(p.BH, p.nkt, p.ns, p.parts, p.rparts, bh, jt) + share;
+              float4* dst = reinterpret_cast<float4*>(p.part + ((slot * 2 + which) * 128 + r) * D + 32 * c);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(__uint_as_float(v[4 * i]) * mul, __uint_as_float(v[4 * i + 1]) * mul,
-                                   __uint_as_float(v[4 * i + 2]) * mul, __uint_as_float(v[4 * i + 3]) * mul);
-          } else if (key_ok) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * mul, __uint_as_float(v[2 * i + 1]) * mul);
-            if (WIN && p.wide) {
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(__uint_as_float(v[4 * i]) * mul, __uint_as_float(v[4 * i + 1]) * mul,
+                                     __uint_as_float(v[4 * i + 2]) * mul, __uint_as_float(v[4 * i + 3]) * mul);
+              continue;
+            }
+            if (key_ok && p.wide) {
               // Whole 32-byte sectors: a warp's stores lie in 32 rows.
+              uint32_t w[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                w[i] = pack_bf16x2(__uint_as_float(v[2 * i]) * mul, __uint_as_float(v[2 * i + 1]) * mul);
               st_global_v8(out + 32 * c, w);
               st_global_v8(out + 32 * c + 16, w + 8);
-            } else {
-              uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              continue;
             }
+          }
+          if (key_ok) {
+            uint4* dst = reinterpret_cast<uint4*>(out + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16x2(__uint_as_float(v[8 * i]) * mul, __uint_as_float(v[8 * i + 1]) * mul),
+                                  pack_bf16x2(__uint_as_float(v[8 * i + 2]) * mul, __uint_as_float(v[8 * i + 3]) * mul),
+                                  pack_bf16x2(__uint_as_float(v[8 * i + 4]) * mul, __uint_as_float(v[8 * i + 5]) * mul),
+                                  pack_bf16x2(__uint_as_float(v[8 * i + 6]) * mul, __uint_as_float(v[8 * i + 7]) * mul));
           }
         }
       }
@@ -640,7 +678,7 @@ __global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS,
     Walk at = walk();
     for (int it = 0; it < (DQ ? n_q : 0); ++it) {
       int hq;
-      const int q0 = at.next_row(hq);
+      const int q0 = next_row(at, it, hq);
       ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_DQ_FULL), it & 1, abort_flag));
       if constexpr (T::SEP_DQ) {
         // The dQ columns are free as soon as they are in registers (four P/dS groups leave 80 of them a thread: the
@@ -874,7 +912,7 @@ __global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS,
         mbar_arrive_expect_tx(bar(T::BAR_QD_FULL + s), 2 * T::TILE_BYTES);
         const uint32_t dst = sbase + T::OFF_QD + s * 2 * T::TILE_BYTES;
         int hq;
-        const int q0 = at.next_row(hq);
+        const int q0 = next_row(at, it, hq);
         for (int b = 0; b < T::NBOX; ++b) {
           tma_load_3d(dst + b * T::BOX_BYTES, &tmQ, bar(T::BAR_QD_FULL + s), 64 * b, q0, hq);
           tma_load_3d(dst + T::TILE_BYTES + b * T::BOX_BYTES, &tmDO, bar(T::BAR_QD_FULL + s), 64 * b, q0, hq);

@@ -8,6 +8,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 #include <utility>
 
 #include "../../include/fa.h"
@@ -232,10 +233,7 @@ fa_status launch_fwd(const void* q, const void* k, const void* v, void* o, float
       !make_map_3d(&mv, v, D, Nk, kvBH, F8))
     return FA_ERR_CUDA;
   if (!set_smem(fa::fa_fwd_kernel<D, F8, EXT, WIN>, T::SMEM_BYTES)) return FA_ERR_CUDA;
-  fa::FwdParams p;
-  p.window = win ? win->window : 0;
-  p.sinks = win ? win->sinks : 0;
-  p.group = win ? win->group : 1;
+  std::conditional_t<WIN, fa::FwdWinParams, fa::FwdParams> p;
   set_ext(p, ext);
   p.descale_q = descale_q;
   p.descale_k = descale_k;
@@ -251,9 +249,13 @@ fa_status launch_fwd(const void* q, const void* k, const void* v, void* o, float
   const int sms = num_sms();
   p.tiles = ((long long)((Nq + 255) / 256) * BH < sms) ? 1 : 2;
   p.nunits = (Nq + 128 * p.tiles - 1) / (128 * p.tiles);
-  p.pair = 0;
-  p.wide = (reinterpret_cast<uintptr_t>(o) & 31u) == 0 ? 1 : 0;
+  long long items = (long long)p.nunits * BH;
   if constexpr (WIN) {
+    p.window = win->window;
+    p.sinks = win->sinks;
+    p.group = win->group;
+    p.wide = (reinterpret_cast<uintptr_t>(o) & 31u) == 0 ? 1 : 0;
+    p.pair = 0;
     // An even number of heads to a key/value head: the two tiles are the same rows of two of them.  They then see the
     // same key tiles, one fewer than two neighbouring row tiles do together.
     const long long paired = (long long)((Nq + 127) / 128) * (BH / 2);
@@ -261,11 +263,11 @@ fa_status launch_fwd(const void* q, const void* k, const void* v, void* o, float
       p.tiles = 2;
       p.pair = 1;
       p.nunits = (Nq + 127) / 128;
+      items = paired;
     }
   }
   p.scale_log2 = scale * 1.4426950408889634f;
   p.causal = causal ? 1 : 0;
-  const long long items = (long long)p.nunits * (p.pair ? BH / 2 : BH);
   if (items > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   const long long blocks = p.tiles == 2 ? (items < sms ? items : sms) : items;
   // The kernel counts K/V loads per CTA in 32-bit integers.
@@ -307,7 +309,7 @@ fa_status launch_bwd(const void* q, const void* k, const void* v, const void* o,
         !set_smem(fa::fa_bwd_main_kernel<D, false>, T::SMEM_BYTES) ||
         (ext && !set_smem(fa::fa_bwd_main_kernel<D, true, true>, T::SMEM_BYTES)))
       return FA_ERR_CUDA;
-    fa::BwdParams p;
+    fa::BwdWinParams p{};  // the window's fields stay unread here
     set_ext(p, ext);
     p.lse = lse;
     p.dvec = dvec;
@@ -375,7 +377,7 @@ fa_status launch_bwd(const void* q, const void* k, const void* v, const void* o,
   return FA_OK;
 }
 
-// How the window backward cuts its key tiles' walks over the query blocks (see BwdParams), and the fp32 partials it
+// How the window backward cuts its key tiles' walks over the query blocks (see BwdWinParams), and the fp32 partials it
 // needs.
 struct WinBwdPlan {
   int ns, parts, plen, rparts;
@@ -451,7 +453,7 @@ fa_status launch_bwd_window(const void* q, const void* k, const void* v, const v
         !make_map_3d(&mdo, dO, D, Nq, BH) || !make_map_3d_f32(&mdq, dq_acc, D, Nq, BH) ||
         !ext_bias_map(&mb, nullptr, Nq, Nk))
       return FA_ERR_CUDA;
-    fa::BwdParams p;
+    fa::BwdWinParams p;
     set_ext(p, nullptr);
     p.lse = lse;
     p.dvec = dvec;

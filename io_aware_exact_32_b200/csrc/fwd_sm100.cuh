@@ -28,6 +28,8 @@
 //    by the sum of those rounded weights, LSE by the exact fp32 sum.
 #pragma once
 
+#include <type_traits>
+
 #include "dropout_sm100.cuh"
 
 namespace fa {
@@ -113,8 +115,13 @@ struct FwdParams {
   int bias_pb, bias_ph;
   int H;
   DropoutCfg drop;
-  // Sliding-window instantiation only: key j is visible to a query at position p iff j <= p and
-  // (j > p - window or j < sinks); query head bh reads key/value head bh / group.
+};
+
+// The sliding-window instantiation's: key j is visible to a query at position p iff j <= p and
+// (j > p - window or j < sinks); query head bh reads key/value head bh / group.  (Types of their own for the window:
+// the mere presence of its fields in FwdParams and FwdItem changed the registers of the bias and dropout
+// instantiation, 32 bytes of spills to 96, and made the bias-only forward 1.13x slower.)
+struct FwdWinParams : FwdParams {
   int window, sinks, group;
   int wide;  // o is 32-byte aligned
   int pair;  // the two tiles of an item: 0 neighbouring row tiles of a head, 1 the same rows of two heads of a group
@@ -123,11 +130,13 @@ struct FwdParams {
 // One work item: the query unit of rows [q0, q0 + 128 tiles) of (batch, head) bh.  n0 / n1: key tiles
 // query tile 0 / 1 must visit (under the causal mask the last key tile of the unit is hidden from
 // tile 0 entirely, so tile 0 skips it); n_kv = max(n0, n1) K/V tiles are streamed.
+struct FwdItem {
+  int bh, q0, n0, n1, n_kv;
+};
 // The window instantiation streams a list of key tiles: the sink tiles 0 .. s - 1, then tiles lo, lo + 1,
 // ...; tile 1 skips the list entries [x0, x1), which its window has left behind.  (Elsewhere the list is
 // 0, 1, 2, ... and nothing is skipped.)
-struct FwdItem {
-  int bh, q0, n0, n1, n_kv;
+struct FwdWinItem : FwdItem {
   int s, lo, x0, x1;
 };
 
@@ -253,7 +262,7 @@ template <int D, bool F8 = false, bool EXT = false, bool WIN = false>
 __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                   const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmB,
-                  const FwdParams p) {
+                  const std::conditional_t<WIN, FwdWinParams, FwdParams> p) {
   static_assert(!(F8 && EXT), "bias and dropout are not combined with FP8 operands");
   static_assert(!(WIN && (F8 || EXT)), "the window is combined with neither FP8 operands nor bias and dropout");
   using T = FwdTraits<D, F8, EXT>;
@@ -271,29 +280,39 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
   // even rounds, backward in odd ones), which evens out the causal work per CTA; with fewer items
   // than CTAs (the split mode) every CTA has exactly one.  Every role walks the same list, and the
   // K/V ring, the Q slots and all barrier phases run on across items.
-  const int n_items = p.nunits * (WIN && p.pair ? p.BH / 2 : p.BH);
+  using Item = std::conditional_t<WIN, FwdWinItem, FwdItem>;
+  // WIN: the two tiles of an item are the same rows of two heads.
+  const bool pair = [&]() -> bool {
+    if constexpr (WIN) return p.pair != 0;
+    return false;
+  }();
+  const int n_items = p.nunits * (pair ? p.BH / 2 : p.BH);
   const int G = gridDim.x;
   // Key tile of entry j of an item's list.
-  auto key_tile = [](const FwdItem& w, int j) -> int { return WIN ? (j < w.s ? j : j - w.s + w.lo) : j; };
+  auto key_tile = [](const Item& w, int j) -> int {
+    if constexpr (WIN) return j < w.s ? j : j - w.s + w.lo;
+    return j;
+  };
   // Whether entry j is a sink tile of at most SHORT visible keys: those are then all its rows see of it, and only
   // they are computed (a tile of a few sinks costs a fifth of a full one).
-  auto is_short = [&](const FwdItem& w, int j) -> bool { return WIN && j < w.s && p.sinks - 128 * j <= T::SHORT; };
+  auto is_short = [&](const Item& w, int j) -> bool {
+    if constexpr (WIN) return j < w.s && p.sinks - 128 * j <= T::SHORT;
+    return false;
+  };
   auto item_at = [&](int r) -> int { return r * G + ((r & 1) ? (G - 1 - (int)blockIdx.x) : (int)blockIdx.x); };
-  auto decode = [&](int i) -> FwdItem {
-    FwdItem w;
-    const int heads = WIN && p.pair ? p.BH / 2 : p.BH;
-    w.bh = WIN && p.pair ? i % heads * 2 : i % heads;
-    const int rank = i / heads;
-    const int unit = p.causal ? (p.nunits - 1 - rank) : rank;
-    w.q0 = unit * (WIN && p.pair ? 128 : 128 * p.tiles);
-    w.s = w.lo = w.x0 = w.x1 = 0;
+  auto decode = [&](int i) -> Item {
+    Item w;
     if constexpr (WIN) {
+      const int heads = pair ? p.BH / 2 : p.BH;
+      w.bh = pair ? i % heads * 2 : i % heads;
+      const int rank = i / heads;
+      w.q0 = (p.nunits - 1 - rank) * (pair ? 128 : 128 * p.tiles);
       const int off = p.Nk - p.Nq, last = p.Nq - 1;
       int hi0, lo1, hi1;
       fwd_window_tiles(w.q0, min(w.q0 + 127, last), off, p.window, w.lo, hi0);
       lo1 = w.lo;
       hi1 = hi0;
-      if (two && !p.pair) fwd_window_tiles(min(w.q0 + 128, last), min(w.q0 + 255, last), off, p.window, lo1, hi1);
+      if (two && !pair) fwd_window_tiles(min(w.q0 + 128, last), min(w.q0 + 255, last), off, p.window, lo1, hi1);
       const int ns = (p.sinks + 127) / 128;
       w.s = min(ns, w.lo);
       w.n_kv = w.s + hi1 - w.lo + 1;
@@ -303,6 +322,10 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
       w.n1 = w.n_kv - (w.x1 - w.x0);
       return w;
     }
+    w.bh = i % p.BH;
+    const int rank = i / p.BH;
+    const int unit = p.causal ? (p.nunits - 1 - rank) : rank;
+    w.q0 = unit * 128 * p.tiles;
     w.n0 = fwd_num_kv_tiles(w.q0, 128, p.Nq, p.Nk, p.causal);
     w.n1 = two ? fwd_num_kv_tiles(w.q0 + 128, 128, p.Nq, p.Nk, p.causal) : w.n0;
     w.n_kv = max(w.n0, w.n1);
@@ -319,7 +342,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
   const bool staged_bias = EXT && p.bias != nullptr;
   // Bias tiles group t consumes in item w, in its order: its key tiles j (two tiles: 0 .. n_t - 1;
   // split: t, t + 2, ...).
-  auto n_bias = [&](const FwdItem& w, int t) { return two ? (t ? w.n1 : w.n0) : (w.n_kv + 1 - t) / 2; };
+  auto n_bias = [&](const Item& w, int t) { return two ? (t ? w.n1 : w.n0) : (w.n_kv + 1 - t) / 2; };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -374,13 +397,17 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
     int cnt = 0;   // S tiles this group has processed in earlier items (barrier phases run on)
     int bcnt = 0;  // staged bias tiles this group has consumed
     for (int it = 0; ok && item_at(it) < n_items; ++it) {
-      const FwdItem w = decode(item_at(it));
-      const int bh = WIN && p.pair ? w.bh + t : w.bh;
-      const int row = w.q0 + (two && !(WIN && p.pair) ? 128 * t : 0) + r;  // query index within the head
+      const Item w = decode(item_at(it));
+      const int bh = pair ? w.bh + t : w.bh;
+      const int row = w.q0 + (two && !pair ? 128 * t : 0) + r;  // query index within the head
       const int n_own = two ? (t ? w.n1 : w.n0) : (w.n_kv + 1 - t) / 2;  // key tiles this group visits
       int kmax = p.Nk - 1;  // last visible key of this row (inclusive)
       if (p.causal) kmax = min(kmax, row + p.Nk - p.Nq);
-      [[maybe_unused]] const int kmin = row + p.Nk - p.Nq - p.window + 1;  // WIN: first key of the window
+      [[maybe_unused]] int kmin = 0, sinks = 0;  // WIN: first key of the window
+      if constexpr (WIN) {
+        kmin = row + p.Nk - p.Nq - p.window + 1;
+        sinks = p.sinks;
+      }
       float m_run = -INFINITY, l_run = 0.f, lr_run = 0.f;
       float scale_log2 = p.scale_log2;
       if constexpr (F8) scale_log2 *= __ldg(p.descale_q + bh) * __ldg(p.descale_k + bh);
@@ -400,7 +427,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
             uint32_t sw[T::SHORT];
             tmem_ld32x32b_x32_wait(lane_addr + colS, sw);
             float* s = reinterpret_cast<float*>(sw);
-            const int n_vis = p.sinks - 128 * j;
+            const int n_vis = sinks - 128 * j;
             float mx = -INFINITY;
 #pragma unroll
             for (int c = 0; c < T::SHORT; ++c) {
@@ -467,7 +494,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         const int lim = kmax - 128 * j;  // keys [0, lim] of this tile are visible
         // WIN: of those, keys [wlo, lim] and keys below slim.
         [[maybe_unused]] const int wlo = kmin - 128 * j;
-        [[maybe_unused]] const int slim = p.sinks - 128 * j;
+        [[maybe_unused]] const int slim = sinks - 128 * j;
         const bool masked = __any_sync(0xffffffffu, lim < 127 || (WIN && wlo > 0 && slim < 128));
         // WIN: the visible keys of 32-key chunk i as bits (one test and one select per score, whatever hides it).
         auto visible = [&](int i) -> uint32_t {
@@ -665,13 +692,17 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             wv[i] = pack_bf16x2(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
-          if (WIN && p.wide) {
-            // Whole 32-byte sectors: a warp's stores lie in 32 rows.
-            if (in_range) {
-              st_global_v8(orow + 32 * c, wv);
-              st_global_v8(orow + 32 * c + 16, wv + 8);
+          if constexpr (WIN) {
+            if (p.wide) {
+              // Whole 32-byte sectors: a warp's stores lie in 32 rows.
+              if (in_range) {
+                st_global_v8(orow + 32 * c, wv);
+                st_global_v8(orow + 32 * c + 16, wv + 8);
+              }
+              return;
             }
-          } else if (in_range) {
+          }
+          if (in_range) {
             uint4* dst = reinterpret_cast<uint4*>(orow + 32 * c);
 #pragma unroll
             for (int i = 0; i < 4; ++i) dst[i] = make_uint4(wv[4 * i], wv[4 * i + 1], wv[4 * i + 2], wv[4 * i + 3]);
@@ -764,7 +795,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
       int L = 0;                // global index of the item's first K/V load
       int cnt0 = 0, cnt1 = 0;   // S tiles of groups 0 / 1 in earlier items (barrier phases run on)
       for (int k = 0; ok && item_at(k) < n_items; ++k) {
-        const FwdItem w = decode(item_at(k));
+        const Item w = decode(item_at(k));
         const int slot = k % T::QSLOTS;
         const uint32_t q_smem[2] = {sbase + T::OFF_Q + (2 * slot) * T::TILE_BYTES,
                                     sbase + T::OFF_Q + (2 * slot + 1) * T::TILE_BYTES};
@@ -814,41 +845,63 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         } else {
           // Two tiles, in the order S0 S1 PV0 S0' PV1 S1' ...; query tile 0 skips the key tiles it
           // cannot see (j >= n0), tile 1 visits all n_kv (WIN: all but [x0, x1)).
-          int v_prev = -1;      // load index of the V tile of tile 1's pending P V
-          int d1 = 0;           // P V products of tile 1 issued
-          bool short1 = false;  // the pending one's tile is short
-          for (int j = 0; ok && j < w.n_kv; ++j) {
-            const int ik = L + 2 * j, iv = ik + 1;
-            const bool has1 = !WIN || j < w.x0 || j >= w.x1;
-            const bool shrt = is_short(w, j);
-            if (!(ok = kv_wait(ik))) break;
-            tc_fence_after();
-            if (j < w.n0) qk(0, q_smem[0], ik, shrt);
-            if (WIN ? v_prev >= 0 : j > 0) {
-              const int done = WIN ? d1 : j - 1;
-              if (done == 0 && !(ok = o_free(1))) break;
-              if (!(ok = pv(1, cnt1 + done, v_prev, done > 0, short1))) break;
-              release(v_prev);
-              ++d1;
-              v_prev = -1;
+          int v_prev = -1;  // load index of the V tile of tile 1's pending P V
+          if constexpr (WIN) {
+            int d1 = 0;           // P V products of tile 1 issued
+            bool short1 = false;  // the pending one's tile is short
+            for (int j = 0; ok && j < w.n_kv; ++j) {
+              const int ik = L + 2 * j, iv = ik + 1;
+              const bool has1 = j < w.x0 || j >= w.x1;
+              const bool shrt = is_short(w, j);
+              if (!(ok = kv_wait(ik))) break;
+              tc_fence_after();
+              if (j < w.n0) qk(0, q_smem[0], ik, shrt);
+              if (v_prev >= 0) {
+                if (d1 == 0 && !(ok = o_free(1))) break;
+                if (!(ok = pv(1, cnt1 + d1, v_prev, d1 > 0, short1))) break;
+                release(v_prev);
+                ++d1;
+                v_prev = -1;
+              }
+              if (has1) qk(1, q_smem[1], ik, shrt);
+              release(ik);
+              if (!(ok = kv_wait(iv))) break;
+              if (j < w.n0) {
+                if (j == 0 && !(ok = o_free(0))) break;
+                if (!(ok = pv(0, cnt0 + j, iv, j > 0, shrt))) break;
+              }
+              short1 = shrt;
+              if (has1)
+                v_prev = iv;
+              else
+                release(iv);
             }
-            if (has1) qk(1, q_smem[1], ik, shrt);
-            release(ik);
-            if (!(ok = kv_wait(iv))) break;
-            if (j < w.n0) {
-              if (j == 0 && !(ok = o_free(0))) break;
-              if (!(ok = pv(0, cnt0 + j, iv, j > 0, shrt))) break;
+            if (ok && v_prev >= 0) {
+              if (d1 == 0) ok = o_free(1);
+              if (ok && (ok = pv(1, cnt1 + d1, v_prev, d1 > 0, short1))) release(v_prev);
             }
-            short1 = shrt;
-            if (has1)
+          } else {
+            for (int j = 0; ok && j < w.n_kv; ++j) {
+              const int ik = L + 2 * j, iv = ik + 1;
+              if (!(ok = kv_wait(ik))) break;
+              tc_fence_after();
+              if (j < w.n0) qk(0, q_smem[0], ik, false);
+              if (j > 0) {
+                if (j == 1 && !(ok = o_free(1))) break;
+                if (!(ok = pv(1, cnt1 + j - 1, v_prev, j - 1 > 0, false))) break;
+                release(v_prev);
+              }
+              qk(1, q_smem[1], ik, false);
+              release(ik);
+              if (!(ok = kv_wait(iv))) break;
+              if (j < w.n0) {
+                if (j == 0 && !(ok = o_free(0))) break;
+                if (!(ok = pv(0, cnt0 + j, iv, j > 0, false))) break;
+              }
               v_prev = iv;
-            else
-              release(iv);
-          }
-          if (ok && (!WIN || v_prev >= 0)) {
-            const int done = WIN ? d1 : w.n_kv - 1;
-            if (done == 0) ok = o_free(1);
-            if (ok && (ok = pv(1, cnt1 + done, v_prev, done > 0, short1))) release(v_prev);
+            }
+            if (ok && w.n_kv == 1) ok = o_free(1);
+            if (ok && (ok = pv(1, cnt1 + w.n_kv - 1, v_prev, w.n_kv - 1 > 0, false))) release(v_prev);
           }
           cnt0 += w.n0;
           cnt1 += w.n1;
@@ -867,7 +920,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
       bool ok = true;
       int L = 0;  // global index of the item's first K/V load
       for (int k = 0; ok && item_at(k) < n_items; ++k) {
-        const FwdItem w = decode(item_at(k));
+        const Item w = decode(item_at(k));
         const int slot = k % T::QSLOTS;
         // The slot's previous item (k - QSLOTS) must have finished its S MMAs.
         if (k >= T::QSLOTS &&
@@ -877,9 +930,11 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
         for (int t = 0; t < p.tiles; ++t)
           for (int b = 0; b < T::NBOX; ++b)
             tma_load_3d(sbase + T::OFF_Q + (2 * slot + t) * T::TILE_BYTES + b * T::BOX_BYTES, &tmQ,
-                        bar(T::BAR_Q_FULL + slot), T::BOX_COLS * b, WIN && p.pair ? w.q0 : w.q0 + 128 * t,
-                        WIN && p.pair ? w.bh + t : w.bh);
+                        bar(T::BAR_Q_FULL + slot), T::BOX_COLS * b, pair ? w.q0 : w.q0 + 128 * t,
+                        pair ? w.bh + t : w.bh);
         ++q_fills[slot];
+        int kv_head = w.bh;
+        if constexpr (WIN) kv_head /= p.group;
         for (int idx = 0; idx < 2 * w.n_kv; ++idx) {
           const int g = L + idx;
           const int s = g % T::NS;
@@ -888,7 +943,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
           const CUtensorMap* map = (idx & 1) ? &tmV : &tmK;
           for (int b = 0; b < T::NBOX; ++b)
             tma_load_3d(sbase + T::OFF_KV + s * T::TILE_BYTES + b * T::BOX_BYTES, map, bar(T::BAR_KV_FULL + s),
-                        T::BOX_COLS * b, 128 * key_tile(w, idx >> 1), WIN ? w.bh / p.group : w.bh);
+                        T::BOX_COLS * b, 128 * key_tile(w, idx >> 1), kv_head);
           issued = g + 1;
         }
         L += 2 * w.n_kv;
@@ -904,7 +959,7 @@ __global__ void __launch_bounds__(FwdTraits<D, F8, EXT>::THREADS, 1)
     if (lane == 0 && staged_bias) {
       bool ok = true;
       for (int k = 0; ok && item_at(k) < n_items; ++k) {
-        const FwdItem w = decode(item_at(k));
+        const Item w = decode(item_at(k));
         const int plane = (w.bh / p.H) * p.bias_pb + (w.bh % p.H) * p.bias_ph;
         const int nb0 = n_bias(w, 0), nb1 = n_bias(w, 1);
         for (int st = 0; ok && st < max(nb0, nb1); ++st) {

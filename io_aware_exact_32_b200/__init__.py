@@ -620,9 +620,22 @@ def fa_get_device_error(stream=None, device=None) -> int:
 
 
 # ------------------------------------------------------------------------------ conveniences
-def _workspace(nbytes: int, device):
+def _on_stream(stream, device):
+    """Context that makes ``stream`` (a torch.cuda.Stream, a raw handle or None: no change) current, for what a call
+    allocates for itself: memory that is given back when the call returns must go back in that stream's order, not while
+    its kernels still run."""
+    if stream is None:
+        return contextlib.nullcontext()
     import torch
-    return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _workspace(nbytes: int, device, stream=None):
+    import torch
+    with _on_stream(stream, device):
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
 
 
 def attention_forward(q, k, v, causal: bool = False, scale=None, stream=None):
@@ -645,7 +658,7 @@ def attention_backward(q, k, v, o, lse, dO, causal: bool = False, scale=None, st
     dk = torch.empty_like(k)
     dv = torch.empty_like(v)
     if workspace is None:
-        workspace = _workspace(fa_bwd_workspace_size(B, H, Nq, d), q.device)
+        workspace = _workspace(fa_bwd_workspace_size(B, H, Nq, d), q.device, stream)
     fa_bwd(q, k, v, o, dO, lse, dq, dk, dv, workspace, causal, scale, stream, deterministic=deterministic)
     return dq, dk, dv
 
@@ -657,7 +670,7 @@ def decode_splitkv(q, k_cache, v_cache, seqlens, scale=None, num_splits: int = 0
     o = torch.empty((B, H, 1, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = _workspace(fa_decode_workspace_size(B, H, k_cache.shape[2], d, num_splits), q.device)
+        workspace = _workspace(fa_decode_workspace_size(B, H, k_cache.shape[2], d, num_splits), q.device, stream)
     fa_decode_splitkv(q, k_cache, v_cache, seqlens, o, lse, workspace, scale, num_splits, stream)
     return o, lse
 
@@ -677,9 +690,10 @@ def attention_forward_fp8(q, k, v, causal: bool = False, scale=None, signs=None,
     and quantised, V is quantised, then fa_fwd_fp8 runs.  Returns (o bf16, lse fp32)."""
     import torch
     B, H, Nq, d = q.shape
-    q8, dq = quantize_fp8(q, signs, hadamard, stream)
-    k8, dk = quantize_fp8(k, signs, hadamard, stream)
-    v8, dv = quantize_fp8(v, None, False, stream)
+    with _on_stream(stream, q.device):
+        q8, dq = quantize_fp8(q, signs, hadamard, stream)
+        k8, dk = quantize_fp8(k, signs, hadamard, stream)
+        v8, dv = quantize_fp8(v, None, False, stream)
     o = torch.empty((B, H, Nq, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     fa_fwd_fp8(q8, k8, v8, dq, dk, dv, o, lse, causal, scale, stream)
@@ -706,7 +720,7 @@ def attention_backward_window(q, k, v, o, lse, dO, window: int, sinks: int = 0, 
     dv = torch.empty_like(v)
     if workspace is None:
         Hkv, Nk = _kv_heads(k, H, B, d)
-        workspace = _workspace(fa_bwd_window_workspace_size(B, H, Hkv, Nq, Nk, d, window, sinks), q.device)
+        workspace = _workspace(fa_bwd_window_workspace_size(B, H, Hkv, Nq, Nk, d, window, sinks), q.device, stream)
     fa_bwd_window(q, k, v, o, dO, lse, dq, dk, dv, workspace, window, sinks, scale, stream)
     return dq, dk, dv
 
@@ -719,7 +733,7 @@ def decode_window(q, k_cache, v_cache, seqlens, window: int, sinks: int = 0, sca
     o = torch.empty((B, H, 1, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = _workspace(fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks), q.device)
+        workspace = _workspace(fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks), q.device, stream)
     fa_decode_window(q, k_cache, v_cache, seqlens, window, sinks, o, lse, workspace, scale, stream)
     return o, lse
 
@@ -756,6 +770,6 @@ def decode_kv4(q, cache, seqlens, window=None, sinks: int = 0, scale=None, strea
     o = torch.empty((B, H, 1, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
     if workspace is None:
-        workspace = _workspace(fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks), q.device)
+        workspace = _workspace(fa_decode_window_workspace_size(B, H, Hkv, Lmax, d, window, sinks), q.device, stream)
     fa_decode_kv4(q, cache, seqlens, window, sinks, o, lse, workspace, scale, stream)
     return o, lse

@@ -622,8 +622,8 @@ def fa_get_device_error(stream=None, device=None) -> int:
 # ------------------------------------------------------------------------------ conveniences
 def _on_stream(stream, device):
     """Context that makes ``stream`` (a torch.cuda.Stream, a raw handle or None: no change) current, for what a call
-    allocates for itself: memory that is given back when the call returns must go back in that stream's order, not while
-    its kernels still run."""
+    allocates or fills for itself: memory that is given back when the call returns must go back in that stream's order,
+    not while its kernels still run, and a fill must be ahead of them."""
     if stream is None:
         return contextlib.nullcontext()
     import torch
@@ -753,8 +753,11 @@ def kv4_read(cache, T: int, starts=None, stream=None):
     the cache's end are zeros."""
     import torch
     B, Hkv, _, half = cache[0].shape
-    k = torch.zeros((B, Hkv, T, 2 * half), dtype=torch.bfloat16, device=cache[0].device)
-    v = torch.zeros_like(k)
+    k = torch.empty((B, Hkv, T, 2 * half), dtype=torch.bfloat16, device=cache[0].device)
+    v = torch.empty_like(k)
+    with _on_stream(stream, k.device):  # the zeros before the read's rows
+        k.zero_()
+        v.zero_()
     fa_kv4_read(cache, k, v, starts, None, stream)
     return k, v
 

@@ -1,5 +1,5 @@
 """The allocating wrappers on a stream that is not the current one (`stream=`): what a call allocates for itself is given
-back in that stream's order."""
+back in that stream's order, and what it fills is filled there."""
 import math
 
 import pytest
@@ -82,6 +82,23 @@ def test_memory_of_a_call_is_not_handed_out_while_it_runs(name, raw, monkeypatch
         for start, size in taken:
             assert t.data_ptr() + t.numel() <= start or start + size <= t.data_ptr()
     side.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_rows_read_back_on_an_idle_stream_while_the_current_one_is_busy(raw):
+    """The zeros past the cache's end are written ahead of the rows, on the call's own stream."""
+    k, v = _bf(2, 2, 50, 64, seed=20), _bf(2, 2, 50, 64, seed=21)
+    cache = _cache(k, v)
+    starts = torch.tensor([45, 3], dtype=torch.int32, device=gc.DEV)
+    want = fa.kv4_read(cache, 20, starts)
+    assert torch.all(want[0][0, :, 5:] == 0) and torch.all(torch.any(want[0][1] != 0, dim=-1))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    torch.cuda._sleep(20_000_000)
+    got = fa.kv4_read(cache, 20, starts, stream=side.cuda_stream if raw else side)
+    torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
 

@@ -224,8 +224,10 @@ FA_API fa_status fa_bwd_deterministic(const void* q, const void* k, const void* 
  * A row that sees no key (p < 0) gets O = 0, LSE = -inf and dq = 0; a key that no row sees gets
  * dk = dv = 0.  A key tile (128 keys) is read whole: K and V must be finite in every tile that a row sees
  * a key of, the hidden keys of those tiles included.  Tiles that no row of a 256-row block sees cost it
- * nothing: the work follows the window, not Nk.  dk and dv are bitwise reproducible; dq sums meet through
- * reduce-adds as in fa_bwd.  Other conventions and limits are those of fa_fwd / fa_bwd.
+ * nothing: the work follows the window, not Nk.  Weights of at most 2^8 (before they are divided by their sum) times V
+ * are summed in fp32: |V| of 2^120 / (keys that the row sees) and more may overflow.  dk and dv are bitwise
+ * reproducible; dq sums meet through reduce-adds as in fa_bwd.  Other conventions and limits are those of
+ * fa_fwd / fa_bwd.
  */
 FA_API fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse,
                                int B, int H, int Hkv, int Nq, int Nk, int d, int window, int sinks,
@@ -349,7 +351,7 @@ FA_API fa_status fa_decode_splitkv_noalloc(const void* q, const void* k_cache, c
  * The visible keys are cut into chunks by the sizes and lengths alone, and merged in a fixed order: the same call
  * gives the same bits, whatever ran before.
  * Up to 8 query heads that share a key/value head are served by one pass over its cache; a larger group
- * takes one pass per 8 heads.  Limits as fa_decode_splitkv.
+ * takes one pass per 8 heads.  Limits as fa_decode_splitkv; sums of weights times V as in fa_fwd_window.
  */
 FA_API size_t fa_decode_window_workspace_size(int B, int H, int Hkv, int Lmax, int d, int window, int sinks);
 FA_API fa_status fa_decode_window(const void* q, const void* k_cache, const void* v_cache, const int* seqlens,
@@ -373,9 +375,10 @@ FA_API fa_status fa_decode_window(const void* q, const void* k_cache, const void
  *   0 <= T <= 2^24, 1 <= Lmax <= 2^24.
  *
  * fa_decode_kv4: fa_decode_window over such a cache (same workspace query); K and V are the values that
- * the codes stand for, of any size: a group's channels keep their accuracy whatever the sizes in other groups, rows and
- * heads, and the LSE does not depend on V.  A non-finite group in a visible row makes the outputs of its key/value
- * head's queries non-finite or meaningless; rows that are not visible are not read.
+ * the codes stand for.  V may use all of bf16's range: a group's channels keep their accuracy whatever the sizes in
+ * other groups, rows and heads, and the LSE does not depend on V.  Entries of q below 2^-27 of their head's largest may
+ * lose bits.  A non-finite group in a visible row makes the outputs of its key/value head's queries non-finite or
+ * meaningless; rows that are not visible are not read.
  */
 FA_API fa_status fa_kv4_write(const void* k, const void* v, void* k_codes, void* k_steps, void* v_codes,
                               void* v_steps, const int* starts, const int* lens, int B, int Hkv, int T,

@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS,
       [[maybe_unused]] const float zscale = p.drop.p8 != 0 ? p.drop.scale : 1.f;
       // 16-column chunks, double-buffered: the load of chunk c+1 is issued right after chunk c
       // has arrived and overlaps its arithmetic (a TMEM load wait covers every load in flight).
+      // Four groups of 80 registers a thread have one buffer: a chunk is loaded once the one before is done.
       constexpr int NCH = T::CW / 16;  // 16-column chunks of this group
       constexpr int NB = T::NCWG == 2 ? 2 : 1;  // buffers
       uint32_t sv[NB][16], dpv[NB][16];
@@ -609,7 +610,7 @@ __global__ void __launch_bounds__(BwdTraits<D, WIN && D == 64 ? 4 : 2>::THREADS,
       mbar_arrive(bar(T::BAR_DS_READY));
     }
     if constexpr (WIN) grid_launch_next();
-    // dK, dV epilogue (group 0 owns it; both groups hold the same key rows).
+    // dK, dV epilogue (group 0 owns it; all groups hold the same key rows).
     if (ok && wg == 0 && n_q > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(T::BAR_ACC_DONE), 0, abort_flag));
     if (!ok) {
       *abort_flag = 1;

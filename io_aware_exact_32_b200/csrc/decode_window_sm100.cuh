@@ -4,7 +4,7 @@
 // Sequence b's query sits at position L - 1 and sees the keys [max(0, L - window), L) and [0, sinks).  These
 // are numbered 0 .. n - 1 (the sinks first); no other cache row is read.  A unit is a sequence's keys under one
 // key/value head and up to 8 of its query heads.  CTAs work on parts of units, and where a unit has several, a second
-// kernel merges their (m, l, O~) partials with the two-block identity of the online softmax:
+// kernel merges their (m, l, O~) or (m, l, O) partials with the two-block identity of the online softmax:
 //  * bf16 cache: parts of at most 1024 keys, which the hardware deals out (the pass is bound by memory, whose
 //    speed differs from SM to SM);
 //  * 4-bit cache: one wave of CTAs, each with an equal share of the list of all units' steps, whose loads run

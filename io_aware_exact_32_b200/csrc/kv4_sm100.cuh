@@ -10,12 +10,14 @@
 // 4 for V), unit u of group g sits at unit position u * (d / 32) + g, a unit's first channel in its lowest
 // nibble.
 //
-// Both kernels only move bytes (2 d one way, 9 d / 16 the other), but at 6.5 TB/s an SM has 4 instructions a clock for
-// 17 channels: a thread takes 16 channels of a row (two lanes a group), so that what is done once a row, a group or a
-// thread is shared by as many channels as its registers hold, and packed fp32 pairs do the arithmetic.  With 8
-// channels a thread a prompt of B4 H8 T2048..4096 d128 took 39 us, write and read back; so it takes 32 to 34 us (each
-// way about 17 us; the issue slots are 63 to 65% and the ALU 52 to 62% busy).  Each row is read and written in whole
-// 32-byte sectors.
+// Both kernels only move bytes, 2.56 a channel.  At 6.5 TB/s an SM moves 23 a clock (at 1.9 GHz), 9 channels, for which it
+// can issue 14 lane-instructions each.  So a thread takes 16 channels of a row (two lanes a group), so that what is done
+// once a row, a group or a thread is shared by as many channels as its registers hold, and packed fp32 pairs do the
+// arithmetic.  With 8 channels a thread a prompt of B4 H8 T2048..4096 d128 took 39 us, write and read back; so it takes
+// 32 to 34 us, each way about 17 us for 8.8 us of bytes.  Per channel the write then issues 14.2 and the read 12.6
+// lane-instructions, those of the threads of rows past the sequences' ends among them: about what the bytes leave time for
+// if no slot stayed empty, and 63 to 65% of the slots (52 to 62% of the ALU) are used.  Each row is read and written in
+// whole 32-byte sectors.
 #pragma once
 
 #include "sm100_ptx.cuh"

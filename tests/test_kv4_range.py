@@ -104,6 +104,14 @@ def test_every_group_of_another_size():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_query_and_key_groups_of_another_size(d):
+    """A group of q 2^-16 of the others against keys 2^16 larger there: its part of the scores counts as much."""
+    q, k, v = _case(1, 4, 2, 300, d, seed=15)
+    _check(_scaled_group(q, 1, -16), _scaled_group(k, 1, 16), v)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("power", [20, 28, 60])
 @pytest.mark.parametrize("at", [0, 3, 64, 500, 999])
 def test_a_row_of_large_values_and_no_weight(at, power):

@@ -14,9 +14,9 @@
 // Bound: HBM (each cache byte serves at most 8 query heads here).  What the 4-bit form costs instead is
 // instructions: at 6.5 TB/s an SM receives 41 codes a clock (at 1.9 GHz) and issues 128 lane-instructions, so a code
 // may cost at most 3.1 of them.  Measured, both kernels of a call: bf16 B32 H32/8 L1024..8192 window 4096 82 us
-// (5.5 TB/s of visible rows), B1 H32/32 L8192 window 1024 13.5 us (launches and one pass's latency); 4 bits B32 H32/8
-// L1024..8192 54 us (3.1 TB/s; the issue slots are 47% and the ALU 40% busy, three CTAs of four warps an SM do
-// not fill more of the gaps, four spill), B1 H16/4 L65536 21 us.
+// (5.5 TB/s of visible rows), B1 H32/32 L8192 window 1024 14 us (launches and one pass's latency); 4 bits B32 H32/8
+// L1024..8192 51 to 56 us (3.0 to 3.3 TB/s; the issue slots are 48% and the ALU 40% busy, three CTAs of four warps an
+// SM do not fill more of the gaps, four spill), B1 H16/4 L65536 22 us.
 // Hence, per warp and tile of 16 keys:
 //  * both products run on mma.sync m16n8k16 with the cache as the 16-row operand and 8 query heads as the
 //    8 columns (S = K q: rows are keys; O^T = V^T p: rows are channels), so a code is unpacked once for up to 8

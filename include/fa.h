@@ -364,6 +364,8 @@ FA_API fa_status fa_decode_window(const void* q, const void* k_cache, const void
  * The d channels of a row form groups of 32.  A group has step = bf16(max |x| / 7) and 4-bit codes
  * clamp(round_half_even(x / step), -7, 7) + 8, and stands for step * (code - 8): 4.5 bits per channel.  A
  * group of zeros reads back as zeros; a group that holds an infinity or NaN reads back as NaN.
+ * bf16's largest finite number stands for a value that rounds to infinity in bf16 (7 steps of 146 * 2^118 each); numbers
+ * below it read back finite.
  *   k_codes, v_codes  [B, Hkv, Lmax, d / 2] bytes;  k_steps, v_steps  [B, Hkv, Lmax, d / 32] bf16
  * Order of the codes in a row: a group's channels are cut into units (8 channels in k_codes, 4 in v_codes);
  * unit u of group g is stored at unit position u * (d / 32) + g, its first channel in its lowest nibble.
